@@ -10,6 +10,9 @@ Layouts (token-major, sequences packed by ``cu_seqlens``):
   q, k [T, H, d_k]   v, o [T, H, d_v]   beta [T, H] fp32
   log_a [T, H, d_k] fp32 (per-channel decay) or [T, H] (scalar decay)
   state [N, H, d_v, d_k] fp32, row = value channel, column = key channel
+8-bit operands (torch.float8_e4m3fn codes with fp32 scales):
+  activations  codes [rows, width], scales [rows, ceil(width / 128)]
+  weights      codes [N, K],        scales [ceil(N / 128), ceil(K / 128)]
 """
 from __future__ import annotations
 
@@ -23,7 +26,10 @@ __all__ = ["PrefillArgs", "PreparedPrefill", "prefill", "kernel_count", "decode_
            "decode_draft", "decode_accept", "PreprocessArgs", "preprocess", "Projections",
            "prefill_from_projections", "cumdecay", "chunk_factors", "workspace_size",
            "projections_workspace_size",
-           "snapshot_count", "snapshot_offsets", "snapshot_offload", "prefill_status", "lib", "GdrError", "LIB_PATH"]
+           "snapshot_count", "snapshot_offsets", "snapshot_offload", "prefill_status",
+           "norm_fp8", "gated_norm_fp8", "quantize_weight_fp8", "linear_fp8", "linear_fp8_status",
+           "PreparedNormFp8", "PreparedGatedNormFp8", "PreparedLinearFp8", "NormFp8Args",
+           "GatedNormFp8Args", "LinearFp8Args", "lib", "GdrError", "LIB_PATH"]
 
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "_build", "libgdr.so")
 
@@ -76,6 +82,40 @@ class PreprocessArgs(ctypes.Structure):
         ("a_bias", ctypes.c_void_p), ("scalar_decay", ctypes.c_int), ("q", ctypes.c_void_p),
         ("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("beta", ctypes.c_void_p),
         ("log_a", ctypes.c_void_p),
+    ]
+
+
+class NormFp8Args(ctypes.Structure):
+    """Mirror of ``gdr_norm_fp8_args`` (include/gdr.h)."""
+    _fields_ = [
+        ("rows", ctypes.c_int64), ("width", ctypes.c_int), ("io_dtype", ctypes.c_int),
+        ("x", ctypes.c_void_p), ("residual", ctypes.c_void_p), ("norm_weight", ctypes.c_void_p),
+        ("norm_eps", ctypes.c_float), ("residual_out", ctypes.c_void_p), ("y", ctypes.c_void_p),
+        ("y_scale", ctypes.c_void_p),
+    ]
+
+
+class GatedNormFp8Args(ctypes.Structure):
+    """Mirror of ``gdr_gated_norm_fp8_args`` (include/gdr.h)."""
+    _fields_ = [
+        ("rows", ctypes.c_int64), ("n_heads", ctypes.c_int), ("d_v", ctypes.c_int),
+        ("o_dtype", ctypes.c_int), ("gate_dtype", ctypes.c_int), ("o", ctypes.c_void_p),
+        ("gate_raw", ctypes.c_void_p), ("norm_weight", ctypes.c_void_p),
+        ("norm_eps", ctypes.c_float), ("y", ctypes.c_void_p), ("y_scale", ctypes.c_void_p),
+    ]
+
+
+LINEAR_MAX_OUTS = 8
+
+
+class LinearFp8Args(ctypes.Structure):
+    """Mirror of ``gdr_linear_fp8_args`` (include/gdr.h)."""
+    _fields_ = [
+        ("rows", ctypes.c_int64), ("n", ctypes.c_int), ("k", ctypes.c_int),
+        ("x", ctypes.c_void_p), ("x_scale", ctypes.c_void_p), ("w", ctypes.c_void_p),
+        ("w_scale", ctypes.c_void_p), ("n_outs", ctypes.c_int),
+        ("out_cols", ctypes.c_int * LINEAR_MAX_OUTS), ("out_dtype", ctypes.c_int * LINEAR_MAX_OUTS),
+        ("out", ctypes.c_void_p * LINEAR_MAX_OUTS),
     ]
 
 
@@ -137,6 +177,16 @@ def lib():
                                            vp, vp]
             L.gdr_decode_accept.restype = i
             L.gdr_decode_accept.argtypes = [i, i, i, i, i, vp, vp, vp, vp]
+            L.gdr_norm_fp8.restype = i
+            L.gdr_norm_fp8.argtypes = [vp, vp]
+            L.gdr_gated_norm_fp8.restype = i
+            L.gdr_gated_norm_fp8.argtypes = [vp, vp]
+            L.gdr_quantize_weight_fp8.restype = i
+            L.gdr_quantize_weight_fp8.argtypes = [i, i, i, vp, vp, vp, vp]
+            L.gdr_linear_fp8.restype = i
+            L.gdr_linear_fp8.argtypes = [vp, vp]
+            L.gdr_linear_fp8_status.restype = i
+            L.gdr_linear_fp8_status.argtypes = [vp]
             _LIB = L
         return _LIB
 
@@ -709,3 +759,280 @@ def snapshot_offload(dev_snapshots, host_snapshots, copy_stream, event, compute_
                                       ctypes.c_void_p(copy_stream.cuda_stream),
                                       ctypes.c_void_p(event.cuda_event)),
            "gdr_snapshot_offload")
+
+
+# ---------------------------------------------------------------------------
+# 8-bit projections (include/gdr.h, "8-bit projections").
+# ---------------------------------------------------------------------------
+FP8_GROUP = 128
+NORM_MAX_WIDTH = 32768
+
+
+def _groups(width: int) -> int:
+    return -(-width // FP8_GROUP)
+
+
+def _need_same_device(*ts):
+    """One launch reads and writes all of them."""
+    dev = None
+    for t in ts:
+        if t is not None:
+            if dev is None:
+                dev = t.device
+            elif t.device != dev:
+                raise ValueError(f"all tensors must be on one device, got {dev} and {t.device}")
+
+
+def _need_aligned16(**ts):
+    for name, t in ts.items():
+        if t is not None and t.numel() and t.data_ptr() % 16:
+            raise ValueError(f"{name} must be 16-byte aligned")
+
+
+def _spans(t):
+    return t.data_ptr(), t.data_ptr() + t.numel() * t.element_size()
+
+
+def _need_apart(outs, ins, same=()):
+    """Outputs overlap neither each other nor an input, except that the pairs
+    of names in ``same`` may be one and the same buffer."""
+    outs = [(n, *_spans(t)) for n, t in outs if t is not None and t.numel()]
+    ins = [(n, *_spans(t)) for n, t in ins if t is not None and t.numel()]
+    for i, (n, a, b) in enumerate(outs):
+        for m, c, d in outs[i + 1:] + ins:
+            if a < d and c < b and not ((n, m) in same and (a, b) == (c, d)):
+                raise ValueError(f"{n} must not overlap {m}")
+
+
+def _check_eps(norm_eps):
+    if not 0.0 <= norm_eps <= 3.0e38:
+        raise ValueError("norm_eps must be >= 0 and finite")
+
+
+class _Prepared:
+    """One library call whose argument block is built and checked once and
+    replayed.  Holds references to every tensor it points at.  ``run()`` enqueues
+    the call on the current stream of the tensors' device (or on ``stream``) and
+    returns the output tensors, whose contents the next ``run()`` overwrites."""
+
+    _what = ""
+
+    def _bind(self, args, keep, outputs):
+        self.args, self._keep, self.outputs = args, keep, outputs
+        self.device = keep[0].device
+        self._index = self.device.index
+        self._fn = getattr(lib(), self._what)
+        self._ref = ctypes.byref(args)
+
+    def run(self, stream=None):
+        if torch.cuda.current_device() != self._index:
+            with torch.cuda.device(self._index):
+                return self._call(stream)
+        return self._call(stream)
+
+    def _call(self, stream):
+        st = stream if stream is not None else torch.cuda.current_stream(self._index)
+        status = self._fn(self._ref, st.cuda_stream)
+        if status != GDR_OK:
+            raise GdrError(status, self._what)
+        return self.outputs
+
+
+class PreparedNormFp8(_Prepared):
+    """``norm_fp8`` over fixed buffers; ``run()`` returns what it returns."""
+
+    _what = "gdr_norm_fp8"
+
+    def __init__(self, x, norm_weight, *, residual=None, norm_eps=1e-6, out=None, out_scale=None,
+                 residual_out=None):
+        _expect_dim(x, 2, "x")
+        rows, width = x.shape
+        dtype = _dtype_code(x)
+        if width % 16 or not 16 <= width <= NORM_MAX_WIDTH:
+            raise ValueError(f"width must be a multiple of 16 up to {NORM_MAX_WIDTH}, got {width}")
+        _expect(norm_weight, (width,), torch.float32, "norm_weight")
+        _expect(residual, (rows, width), x.dtype, "residual")
+        if residual is None and residual_out is not None:
+            raise ValueError("residual_out needs a residual")
+        _expect(residual_out, (rows, width), x.dtype, "residual_out")
+        _expect(out, (rows, width), torch.float8_e4m3fn, "out")
+        _expect(out_scale, (rows, _groups(width)), torch.float32, "out_scale")
+        _check_eps(norm_eps)
+        _need_cuda(x, norm_weight, residual, out, out_scale, residual_out)
+        _need_same_device(x, norm_weight, residual, out, out_scale, residual_out)
+        dev = x.device
+        if out is None:
+            out = torch.empty(rows, width, dtype=torch.float8_e4m3fn, device=dev)
+        if out_scale is None:
+            out_scale = torch.empty(rows, _groups(width), dtype=torch.float32, device=dev)
+        if residual is not None and residual_out is None:
+            residual_out = torch.empty_like(x)
+        _need_aligned16(x=x, norm_weight=norm_weight, residual=residual, residual_out=residual_out,
+                        out=out)
+        _need_apart([("residual_out", residual_out), ("out", out), ("out_scale", out_scale)],
+                    [("x", x), ("residual", residual), ("norm_weight", norm_weight)],
+                    same={("residual_out", "x"), ("residual_out", "residual")})
+        a = NormFp8Args()
+        a.rows, a.width, a.io_dtype = rows, width, dtype
+        a.x, a.norm_weight, a.norm_eps = x.data_ptr(), norm_weight.data_ptr(), float(norm_eps)
+        if residual is not None:
+            a.residual, a.residual_out = residual.data_ptr(), residual_out.data_ptr()
+        a.y, a.y_scale = out.data_ptr(), out_scale.data_ptr()
+        outputs = (out, out_scale) if residual is None else (out, out_scale, residual_out)
+        self._bind(a, (x, norm_weight, residual, out, out_scale, residual_out), outputs)
+
+
+def norm_fp8(x, norm_weight, *, residual=None, norm_eps=1e-6, out=None, out_scale=None,
+             residual_out=None):
+    """RMSNorm of the residual stream, with the residual's addition, as 8-bit codes.
+
+    h = x + residual (fp32), y = h / sqrt(mean h^2 + norm_eps) * norm_weight.
+    x, residual [rows, width] bf16 or fp32, norm_weight [width] fp32, width a
+    multiple of 16.  Returns (codes [rows, width] e4m3, scales [rows,
+    ceil(width / 128)] fp32) and, with a residual, h rounded to x's dtype
+    (``residual_out``, which may be x or residual itself).
+    """
+    return PreparedNormFp8(x, norm_weight, residual=residual, norm_eps=norm_eps, out=out,
+                           out_scale=out_scale, residual_out=residual_out).run()
+
+
+class PreparedGatedNormFp8(_Prepared):
+    """``gated_norm_fp8`` over fixed buffers; ``run()`` returns what it returns."""
+
+    _what = "gdr_gated_norm_fp8"
+
+    def __init__(self, o, gate_raw, norm_weight, *, norm_eps=1e-6, out=None, out_scale=None):
+        _expect_dim(o, 3, "o")
+        rows, H, d = o.shape
+        if d not in (64, 128):
+            raise ValueError(f"d_v must be 64 or 128, got {d}")
+        if H < 1:
+            raise ValueError("o needs at least one head")
+        _expect(gate_raw, (rows, H, d), None, "gate_raw")
+        _expect(norm_weight, (d,), torch.float32, "norm_weight")
+        _expect(out, (rows, H * d), torch.float8_e4m3fn, "out")
+        _expect(out_scale, (rows, _groups(H * d)), torch.float32, "out_scale")
+        _check_eps(norm_eps)
+        a = GatedNormFp8Args()
+        a.rows, a.n_heads, a.d_v = rows, H, d
+        a.o_dtype, a.gate_dtype = _dtype_code(o), _dtype_code(gate_raw)
+        _need_cuda(o, gate_raw, norm_weight, out, out_scale)
+        _need_same_device(o, gate_raw, norm_weight, out, out_scale)
+        if out is None:
+            out = torch.empty(rows, H * d, dtype=torch.float8_e4m3fn, device=o.device)
+        if out_scale is None:
+            out_scale = torch.empty(rows, _groups(H * d), dtype=torch.float32, device=o.device)
+        _need_aligned16(o=o, gate_raw=gate_raw, norm_weight=norm_weight, out=out)
+        _need_apart([("out", out), ("out_scale", out_scale)],
+                    [("o", o), ("gate_raw", gate_raw), ("norm_weight", norm_weight)])
+        a.o, a.gate_raw, a.norm_weight = o.data_ptr(), gate_raw.data_ptr(), norm_weight.data_ptr()
+        a.norm_eps = float(norm_eps)
+        a.y, a.y_scale = out.data_ptr(), out_scale.data_ptr()
+        self._bind(a, (o, gate_raw, norm_weight, out, out_scale), (out, out_scale))
+
+
+def gated_norm_fp8(o, gate_raw, norm_weight, *, norm_eps=1e-6, out=None, out_scale=None):
+    """The output epilogue with 8-bit codes as its result: per token and head
+    y = o / sqrt(mean o^2 + norm_eps) * norm_weight * sigmoid(gate_raw).
+
+    o [rows, H, d_v] (a ``prefill``'s or a ``decode_step``'s output without the
+    epilogue), gate_raw [rows, H, d_v], each bf16 or fp32; norm_weight [d_v] fp32.
+    Returns (codes [rows, H * d_v] e4m3, scales [rows, ceil(H * d_v / 128)]).
+    """
+    return PreparedGatedNormFp8(o, gate_raw, norm_weight, norm_eps=norm_eps, out=out,
+                                out_scale=out_scale).run()
+
+
+def quantize_weight_fp8(w, *, out=None, out_scale=None):
+    """A weight matrix w [N, K] (bf16 or fp32, K a multiple of 16) as e4m3 codes
+    [N, K] and one fp32 scale per 128 x 128 block [ceil(N / 128), ceil(K / 128)]."""
+    _expect_dim(w, 2, "w")
+    n, k = w.shape
+    dtype = _dtype_code(w)
+    if k % 16 or k < 16:
+        raise ValueError(f"K must be a positive multiple of 16, got {k}")
+    _expect(out, (n, k), torch.float8_e4m3fn, "out")
+    _expect(out_scale, (_groups(n), _groups(k)), torch.float32, "out_scale")
+    _need_cuda(w, out, out_scale)
+    _need_same_device(w, out, out_scale)
+    if out is None:
+        out = torch.empty(n, k, dtype=torch.float8_e4m3fn, device=w.device)
+    if out_scale is None:
+        out_scale = torch.empty(_groups(n), _groups(k), dtype=torch.float32, device=w.device)
+    _need_aligned16(w=w, out=out)
+    _need_apart([("out", out), ("out_scale", out_scale)], [("w", w)])
+    with torch.cuda.device(w.device):
+        _check(lib().gdr_quantize_weight_fp8(n, k, dtype, _ptr(w), _ptr(out), _ptr(out_scale),
+                                             _stream(w.device)), "gdr_quantize_weight_fp8")
+    return out, out_scale
+
+
+class PreparedLinearFp8(_Prepared):
+    """``linear_fp8`` over fixed buffers; ``run()`` returns what it returns."""
+
+    _what = "gdr_linear_fp8"
+
+    def __init__(self, x, x_scale, w, w_scale, *, splits=None, out_dtype=torch.bfloat16, out=None):
+        _expect_dim(x, 2, "x")
+        _expect_dim(w, 2, "w")
+        rows, k = x.shape
+        n = w.shape[0]
+        if k % 16 or k < 16:
+            raise ValueError(f"K must be a positive multiple of 16, got {k}")
+        if n < 1:
+            raise ValueError("w needs at least one row")
+        _expect(x, (rows, k), torch.float8_e4m3fn, "x")
+        _expect(x_scale, (rows, _groups(k)), torch.float32, "x_scale")
+        _expect(w, (n, k), torch.float8_e4m3fn, "w")
+        _expect(w_scale, (_groups(n), _groups(k)), torch.float32, "w_scale")
+        cols = [n] if splits is None else [int(c) for c in splits]
+        if not 1 <= len(cols) <= LINEAR_MAX_OUTS or any(c < 1 for c in cols) or sum(cols) != n:
+            raise ValueError(f"splits must be 1 to {LINEAR_MAX_OUTS} positive widths that add up to {n}")
+        dtypes = [out_dtype] * len(cols) if isinstance(out_dtype, torch.dtype) else list(out_dtype)
+        if len(dtypes) != len(cols) or any(t not in (torch.bfloat16, torch.float32) for t in dtypes):
+            raise TypeError("out_dtype must be bfloat16 or float32, or one of them for each split")
+        outs = [None] * len(cols) if out is None else [out] if torch.is_tensor(out) else list(out)
+        if len(outs) != len(cols):
+            raise ValueError("out must hold one tensor for each split")
+        for i, t in enumerate(outs):
+            _expect(t, (rows, cols[i]), dtypes[i], f"out[{i}]")
+        _need_cuda(x, x_scale, w, w_scale, *outs)
+        _need_same_device(x, x_scale, w, w_scale, *outs)
+        outs = [torch.empty(rows, c, dtype=t, device=x.device) if o is None else o
+                for o, c, t in zip(outs, cols, dtypes)]
+        _need_aligned16(x=x, w=w)
+        _need_apart([(f"out[{i}]", t) for i, t in enumerate(outs)],
+                    [("x", x), ("x_scale", x_scale), ("w", w), ("w_scale", w_scale)])
+        a = LinearFp8Args()
+        a.rows, a.n, a.k = rows, n, k
+        a.x, a.x_scale, a.w, a.w_scale = (x.data_ptr(), x_scale.data_ptr(), w.data_ptr(),
+                                          w_scale.data_ptr())
+        a.n_outs = len(cols)
+        for i, t in enumerate(outs):
+            a.out_cols[i], a.out_dtype[i], a.out[i] = cols[i], _dtype_code(t), t.data_ptr()
+        self._bind(a, (x, x_scale, w, w_scale, *outs), outs[0] if splits is None else tuple(outs))
+
+
+def linear_fp8(x, x_scale, w, w_scale, *, splits=None, out_dtype=torch.bfloat16, out=None):
+    """Matrix product y = x w^T of 8-bit operands, rounded once to ``out_dtype``.
+
+    x [M, K] e4m3 with x_scale [M, ceil(K / 128)] (``norm_fp8``,
+    ``gated_norm_fp8``), w [N, K] e4m3 with w_scale [ceil(N / 128),
+    ceil(K / 128)] (``quantize_weight_fp8``).  Returns y [M, N].  With
+    ``splits`` (up to 8 widths that add up to N) w is a stack of projections and
+    the result is a tuple of dense tensors, one for each width; ``out_dtype`` may
+    then be a list: ``splits=(H * d, H * d, H * d, H * d, H)`` with
+    ``out_dtype=(bf16, bf16, bf16, f32, f32)`` gives x_q, x_k, x_v, a_raw and
+    beta_raw as ``prefill_from_projections`` and ``preprocess`` take them (after a
+    ``view`` of the first four as [T, H, d]).
+    """
+    return PreparedLinearFp8(x, x_scale, w, w_scale, splits=splits, out_dtype=out_dtype,
+                             out=out).run()
+
+
+def linear_fp8_status(device=None) -> None:
+    """Raise if a ``linear_fp8`` kernel on ``device`` gave up a bounded wait since
+    the last call of this function.  Synchronises the current stream."""
+    with torch.cuda.device(device):
+        st = torch.cuda.current_stream()
+        _check(lib().gdr_linear_fp8_status(ctypes.c_void_p(st.cuda_stream)), "gdr_linear_fp8_status")

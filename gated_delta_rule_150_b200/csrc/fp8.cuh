@@ -1,0 +1,97 @@
+// fp8.cuh -- the 8-bit format shared by the norm, gated-norm and weight
+// kernels: e4m3 codes in groups of 128 channels with one fp32 scale each,
+// scale = max(max |y|, 1e-12) / 448, code = y / scale rounded to nearest even.
+#pragma once
+
+#include <cstdint>
+#include <cuda_bf16.h>
+#include <cuda_fp8.h>
+
+namespace gdr {
+
+constexpr int kFp8Group = 128;
+
+inline int fp8_groups(int64_t width) { return (int)((width + kFp8Group - 1) / kFp8Group); }
+
+// Eight consecutive values of a row ("octet"): one or two 16-byte accesses.
+template <typename T>
+struct Octet;
+
+template <>
+struct Octet<__nv_bfloat16> {
+    uint4 raw;
+    __device__ __forceinline__ void zero() { raw = make_uint4(0u, 0u, 0u, 0u); }
+    __device__ __forceinline__ void load(const __nv_bfloat16* p) {
+        raw = __ldcs(reinterpret_cast<const uint4*>(p));
+    }
+    __device__ __forceinline__ void to_float(float (&f)[8]) const {
+        const uint32_t u[4] = {raw.x, raw.y, raw.z, raw.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            f[2 * i] = __uint_as_float(u[i] << 16);
+            f[2 * i + 1] = __uint_as_float(u[i] & 0xffff0000u);
+        }
+    }
+    static __device__ __forceinline__ void store(__nv_bfloat16* p, const float (&f)[8]) {
+        uint32_t u[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const __nv_bfloat162 b = __floats2bfloat162_rn(f[2 * i], f[2 * i + 1]);
+            u[i] = *reinterpret_cast<const uint32_t*>(&b);
+        }
+        *reinterpret_cast<uint4*>(p) = make_uint4(u[0], u[1], u[2], u[3]);
+    }
+};
+
+template <>
+struct Octet<float> {
+    float4 lo, hi;
+    __device__ __forceinline__ void zero() { lo = hi = make_float4(0.f, 0.f, 0.f, 0.f); }
+    __device__ __forceinline__ void load(const float* p) {
+        lo = __ldcs(reinterpret_cast<const float4*>(p));
+        hi = __ldcs(reinterpret_cast<const float4*>(p) + 1);
+    }
+    __device__ __forceinline__ void to_float(float (&f)[8]) const {
+        f[0] = lo.x; f[1] = lo.y; f[2] = lo.z; f[3] = lo.w;
+        f[4] = hi.x; f[5] = hi.y; f[6] = hi.z; f[7] = hi.w;
+    }
+    static __device__ __forceinline__ void store(float* p, const float (&f)[8]) {
+        reinterpret_cast<float4*>(p)[0] = make_float4(f[0], f[1], f[2], f[3]);
+        reinterpret_cast<float4*>(p)[1] = make_float4(f[4], f[5], f[6], f[7]);
+    }
+};
+
+// max |f| as its bit pattern: ordered like the values, infinity above every
+// finite value and NaN above infinity, so a maximum of patterns keeps a NaN
+// (fmaxf would drop it).
+__device__ __forceinline__ uint32_t abs_bits_max(const float (&f)[8]) {
+    uint32_t m = 0u;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) m = max(m, __float_as_uint(f[i]) & 0x7fffffffu);
+    return m;
+}
+
+// Maximum over the 16 lanes (an aligned half warp) that hold one group.
+__device__ __forceinline__ uint32_t half_warp_max(uint32_t m) {
+#pragma unroll
+    for (int s = 8; s > 0; s >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, s));
+    return m;
+}
+
+__device__ __forceinline__ float fp8_scale(uint32_t amax_bits) {
+    const float a = __uint_as_float(amax_bits);
+    return (a < 1e-12f ? 1e-12f : a) / 448.f;      // a NaN stays
+}
+
+// Codes of an octet: y * (1 / scale), saturating (a rounding of 1 / scale may
+// lift the largest value an fp32 step above 448).
+__device__ __forceinline__ uint2 fp8_codes(const float (&y)[8], float inv_scale) {
+    uint32_t h[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        h[i] = __nv_cvt_float2_to_fp8x2(make_float2(y[2 * i] * inv_scale, y[2 * i + 1] * inv_scale),
+                                        __NV_SATFINITE, __NV_E4M3);
+    return make_uint2(h[0] | (h[1] << 16), h[2] | (h[3] << 16));
+}
+
+}  // namespace gdr

@@ -25,6 +25,8 @@ gdr_status from_cuda(cudaError_t e) {
 }
 
 bool supported_width(int d) { return d == 64 || d == 128; }
+bool valid_dtype(gdr_dtype dt) { return dt == GDR_BF16 || dt == GDR_F32; }
+bool valid_eps(float eps) { return eps >= 0.f && eps <= 3.0e38f; }
 
 // Shared checks of the prefill arguments that do not depend on outputs.
 gdr_status check_prefill_inputs(const gdr_prefill_args* a) {
@@ -492,6 +494,69 @@ gdr_status gdr_decode_accept(int batch, int n_tokens, int n_heads, int d_k, int 
     return from_cuda(gdr::launch_decode_accept(batch, n_tokens, n_heads, d_k, d_v, n_accept,
                                                token_states, state,
                                                static_cast<cudaStream_t>(stream)));
+}
+
+gdr_status gdr_norm_fp8(const gdr_norm_fp8_args* a, void* stream) {
+    if (!a) return GDR_ERR_INVALID_ARG;
+    if (a->rows < 0 || a->rows > (int64_t)INT32_MAX || a->width <= 0) return GDR_ERR_INVALID_ARG;
+    if (!valid_dtype(a->io_dtype) || !valid_eps(a->norm_eps)) return GDR_ERR_INVALID_ARG;
+    if (a->width % 16 != 0 || a->width > GDR_NORM_MAX_WIDTH) return GDR_ERR_UNSUPPORTED;
+    if (a->residual_out && !a->residual) return GDR_ERR_INVALID_ARG;
+    if (a->rows == 0) return GDR_OK;
+    const void* v16[] = {a->x, a->norm_weight, a->y};
+    for (const void* p : v16)
+        if (!p || !aligned16(p)) return GDR_ERR_INVALID_ARG;
+    if (!aligned16(a->residual) || !aligned16(a->residual_out)) return GDR_ERR_INVALID_ARG;
+    if (!a->y_scale || !aligned4(a->y_scale)) return GDR_ERR_INVALID_ARG;
+    return from_cuda(gdr::launch_norm_fp8(*a, static_cast<cudaStream_t>(stream)));
+}
+
+gdr_status gdr_gated_norm_fp8(const gdr_gated_norm_fp8_args* a, void* stream) {
+    if (!a) return GDR_ERR_INVALID_ARG;
+    if (a->rows < 0 || a->rows > (int64_t)INT32_MAX || a->n_heads <= 0 || a->d_v <= 0)
+        return GDR_ERR_INVALID_ARG;
+    if (!valid_dtype(a->o_dtype) || !valid_dtype(a->gate_dtype) || !valid_eps(a->norm_eps))
+        return GDR_ERR_INVALID_ARG;
+    if (!supported_width(a->d_v)) return GDR_ERR_UNSUPPORTED;
+    if ((int64_t)a->n_heads * a->d_v > (int64_t)INT32_MAX) return GDR_ERR_INVALID_ARG;
+    if (a->rows == 0) return GDR_OK;
+    const void* v16[] = {a->o, a->gate_raw, a->norm_weight, a->y};
+    for (const void* p : v16)
+        if (!p || !aligned16(p)) return GDR_ERR_INVALID_ARG;
+    if (!a->y_scale || !aligned4(a->y_scale)) return GDR_ERR_INVALID_ARG;
+    return from_cuda(gdr::launch_gated_norm_fp8(*a, static_cast<cudaStream_t>(stream)));
+}
+
+gdr_status gdr_quantize_weight_fp8(int n, int k, gdr_dtype w_dtype, const void* w, void* codes,
+                                   float* scales, void* stream) {
+    if (n < 0 || k <= 0 || !valid_dtype(w_dtype)) return GDR_ERR_INVALID_ARG;
+    if (k % 16 != 0) return GDR_ERR_UNSUPPORTED;
+    if (n == 0) return GDR_OK;
+    if (!w || !aligned16(w) || !codes || !aligned16(codes) || !scales || !aligned4(scales))
+        return GDR_ERR_INVALID_ARG;
+    return from_cuda(gdr::launch_quantize_weight_fp8(n, k, w_dtype, w, codes, scales,
+                                                     static_cast<cudaStream_t>(stream)));
+}
+
+gdr_status gdr_linear_fp8(const gdr_linear_fp8_args* a, void* stream) {
+    if (!a) return GDR_ERR_INVALID_ARG;
+    if (a->rows < 0 || a->rows > (int64_t)INT32_MAX || a->n <= 0 || a->k <= 0)
+        return GDR_ERR_INVALID_ARG;
+    if (a->k % 16 != 0) return GDR_ERR_UNSUPPORTED;
+    if (a->n_outs < 1 || a->n_outs > GDR_LINEAR_MAX_OUTS) return GDR_ERR_INVALID_ARG;
+    int64_t cols = 0;
+    for (int i = 0; i < a->n_outs; ++i) {
+        if (a->out_cols[i] <= 0 || !valid_dtype(a->out_dtype[i])) return GDR_ERR_INVALID_ARG;
+        cols += a->out_cols[i];
+    }
+    if (cols != a->n) return GDR_ERR_INVALID_ARG;
+    if (a->rows == 0) return GDR_OK;
+    if (!a->x || !aligned16(a->x) || !a->w || !aligned16(a->w)) return GDR_ERR_INVALID_ARG;
+    if (!a->x_scale || !aligned4(a->x_scale) || !a->w_scale || !aligned4(a->w_scale))
+        return GDR_ERR_INVALID_ARG;
+    for (int i = 0; i < a->n_outs; ++i)
+        if (!a->out[i] || !aligned_elem(a->out[i], a->out_dtype[i])) return GDR_ERR_INVALID_ARG;
+    return from_cuda(gdr::launch_linear_fp8(*a, static_cast<cudaStream_t>(stream)));
 }
 
 }  // extern "C"

@@ -207,6 +207,15 @@ cudaError_t launch_decode_draft(int B, int K, int H, int dk, int dv, gdr_dtype d
 cudaError_t launch_decode_accept(int B, int K, int H, int dk, int dv, const int32_t* n_accept,
                                  const float* token_states, float* state, cudaStream_t st);
 
+cudaError_t launch_norm_fp8(const gdr_norm_fp8_args& a, cudaStream_t st);
+
+cudaError_t launch_gated_norm_fp8(const gdr_gated_norm_fp8_args& a, cudaStream_t st);
+
+cudaError_t launch_quantize_weight_fp8(int n, int k, gdr_dtype dt, const void* w, void* codes,
+                                       float* scales, cudaStream_t st);
+
+cudaError_t launch_linear_fp8(const gdr_linear_fp8_args& a, cudaStream_t st);
+
 // Device helper: slot -> (sequence, chunk index).  f(n) = floor(cu[n]/64) + n is
 // strictly increasing, so the owner of slot j is the largest n with f(n) <= j.
 // Returns false if the slot holds no chunk.

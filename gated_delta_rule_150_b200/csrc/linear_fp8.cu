@@ -1,0 +1,388 @@
+// linear_fp8.cu -- y = (x codes * x scales) (w codes * w scales)^T with e4m3
+// codes, one fp32 scale per token and 128 channels (x) and per 128 x 128 block
+// (w):
+//     y[m, c] = sum_b sx[m, b] sw[c / 128, b] sum_{j in b} x[m, j] w[c, j].
+//
+// The scales differ from one 128-channel group to the next, so the tensor core
+// sums one group (four K = 32 MMAs) into a TMEM accumulator, and the epilogue
+// warps add it into fp32 registers with its factor while the next group's MMAs
+// run into a second accumulator.
+#include <cstring>
+#include <cuda.h>
+
+#include "fp8.cuh"
+#include "internal.h"
+#include "sm100.cuh"
+
+namespace gdr {
+namespace {
+
+// Set by a kernel that gave up a bounded wait; read and cleared by
+// gdr_linear_fp8_status.
+__device__ uint32_t g_linear_error;
+
+// The output's column ranges: columns begin[i] .. begin[i + 1] - 1 go to the
+// dense tensor ptr[i].
+struct OutRanges {
+    int n_outs;
+    int begin[GDR_LINEAR_MAX_OUTS + 1];
+    int f32[GDR_LINEAR_MAX_OUTS];
+    void* ptr[GDR_LINEAR_MAX_OUTS];
+};
+
+// One output column: where its tensor's row 0 holds it, and that tensor's row
+// length (0: past the last column).
+struct OutColumn {
+    void* p;
+    int pitch;
+    int f32;
+    __device__ __forceinline__ OutColumn(const OutRanges& r, int c) : p(nullptr), pitch(0), f32(0) {
+        for (int i = 0; i < r.n_outs; ++i)
+            if (c >= r.begin[i] && c < r.begin[i + 1]) {
+                pitch = r.begin[i + 1] - r.begin[i];
+                f32 = r.f32[i];
+                const int64_t off = c - r.begin[i];
+                p = f32 ? (void*)((float*)r.ptr[i] + off) : (void*)((__nv_bfloat16*)r.ptr[i] + off);
+            }
+    }
+    __device__ __forceinline__ void store(int64_t row, float v) const {
+        if (f32) ((float*)p)[row * pitch] = v;
+        else ((__nv_bfloat16*)p)[row * pitch] = __float2bfloat16_rn(v);
+    }
+};
+
+// A wait that ends: true once the phase completed, false when another role of
+// the CTA gave up or the limit ran out (then the error word is set).
+__device__ __forceinline__ bool wait_or_give_up(uint64_t* bar, uint32_t parity, volatile int* gave_up) {
+    const uint32_t a = smem_u32(bar);
+    if (mbar_try_wait(a, parity)) return true;
+    const uint64_t t0 = global_timer_ns();
+    while (true) {
+        if (mbar_try_wait(a, parity)) return true;
+        if (*gave_up) return false;
+        if (global_timer_ns() - t0 > kWaitLimitNs) {
+            *gave_up = 1;
+            atomicOr(&g_linear_error, 1u);
+            return false;
+        }
+    }
+}
+
+__device__ __forceinline__ void mbar_arrive(uint64_t* bar) {
+    asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_u32(bar)) : "memory");
+}
+
+__device__ __forceinline__ void cluster_sync() {
+    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+
+// Read a float of CTA `rank` of the cluster at the place `addr` of this CTA.
+__device__ __forceinline__ float ld_cluster(uint32_t addr, uint32_t rank) {
+    uint32_t at;
+    float v;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"(addr), "r"(rank));
+    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(at) : "memory");
+    return v;
+}
+
+// ---------------------------------------------------------------------------
+// Few tokens: the weights take the MMA's 128-row side and BN tokens its other
+// side, so a decode step's few tokens do not leave the tensor core's rows empty
+// and every weight is fetched once per BN tokens.  A cluster of `split` CTAs
+// shares one 128-column tile: each sums a range of the K groups, and the parts
+// meet through distributed shared memory in rank order (no atomics, no
+// workspace).
+//   warps 0-3   a thread owns an output column, BN fp32 sums (one per token)
+//   warp 4      TMA loads (one lane)
+//   warp 5      TMEM allocation, MMAs (one lane)
+// ---------------------------------------------------------------------------
+constexpr int kFewThreads = 192;
+
+template <int BN>
+struct FewLayout {
+    static constexpr uint32_t kStageBytes = 16384u + BN * 128u;
+    static constexpr int kStages = BN <= 32 ? 6 : BN <= 64 ? 5 : 4;
+    static constexpr uint32_t kFactors = kStages * kStageBytes;         // 4 warps x 2 x BN floats
+    static constexpr uint32_t kBytes = kFactors + 4u * 2u * BN * 4u;
+    static constexpr uint32_t kDynBytes = kBytes + 1024u;               // 1024-byte alignment
+    static constexpr uint32_t kTmemCols = 2 * BN < 32 ? 32 : 2 * BN;
+    static_assert((uint32_t)BN * 512u <= kFactors, "the parts take the stages' place");
+};
+
+template <int BN>
+__global__ void __launch_bounds__(kFewThreads)
+linear_few_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUtensorMap map_x,
+                  const float* __restrict__ sx, const float* __restrict__ sw, int M, int groups,
+                  int split, const __grid_constant__ OutRanges out) {
+    using Lay = FewLayout<BN>;
+    constexpr int ST = Lay::kStages;
+    extern __shared__ uint8_t dyn[];
+    uint8_t* smem = align_smem<1024>(dyn);
+    __shared__ uint64_t full[ST], empty[ST], acc_full[2], acc_empty[2], drained;
+    __shared__ uint32_t tmem_slot;
+    __shared__ int gave_up;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int tile = blockIdx.x / split, part = blockIdx.x - tile * split;
+    const int n0 = tile * 128, m0 = blockIdx.y * BN;
+    const int g0 = (int)((int64_t)groups * part / split), g1 = (int)((int64_t)groups * (part + 1) / split);
+    const int count = g1 - g0;
+
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < ST; ++i) { mbar_init(&full[i], 1); mbar_init(&empty[i], 1); }
+        for (int i = 0; i < 2; ++i) { mbar_init(&acc_full[i], 1); mbar_init(&acc_empty[i], 4); }
+        mbar_init(&drained, 1);
+        gave_up = 0;
+        fence_mbar_init();
+    }
+    if (warp == 5) tmem_alloc(&tmem_slot, Lay::kTmemCols);
+    tc_fence_before_sync();
+    __syncthreads();
+    tc_fence_after_sync();
+    const uint32_t tmem = tmem_slot;
+    pdl_wait();
+    pdl_launch_dependents();
+
+    float acc[BN];
+    if (warp == 4) {
+        if (lane == 0) {
+            int issued = 0;
+            for (; issued < count; ++issued) {
+                const int s = issued % ST;
+                if (issued >= ST && !wait_or_give_up(&empty[s], ((issued / ST) & 1) ^ 1, &gave_up)) break;
+                uint8_t* st = smem + s * Lay::kStageBytes;
+                mbar_arrive_expect_tx(&full[s], Lay::kStageBytes);
+                tma_load_2d(st, &map_w, (g0 + issued) * kFp8Group, n0, &full[s]);
+                tma_load_2d(st + 16384, &map_x, (g0 + issued) * kFp8Group, m0, &full[s]);
+            }
+            // gave up: no copy may still be in flight when the CTA ends
+            if (*(volatile int*)&gave_up)
+                for (int i = issued < ST ? 0 : issued - ST; i < issued; ++i)
+                    mbar_wait(&full[i % ST], (i / ST) & 1);
+        }
+    } else if (warp == 5) {
+        if (lane == 0) {
+            constexpr uint32_t idesc = idesc_e4m3_f32(128, BN);
+            for (int i = 0; i < count; ++i) {
+                const int s = i % ST, buf = i & 1;
+                if (i >= 2 && !wait_or_give_up(&acc_empty[buf], ((i >> 1) & 1) ^ 1, &gave_up)) break;
+                if (!wait_or_give_up(&full[s], (i / ST) & 1, &gave_up)) break;
+                tc_fence_after_sync();
+                const uint32_t a = smem_u32(smem + s * Lay::kStageBytes);
+#pragma unroll
+                for (int j = 0; j < 4; ++j)      // 32 codes = 32 bytes = 16 of the descriptor's 2-byte columns
+                    mma_e4m3(tmem + buf * BN, sw128_desc(a, 128, 0, 16 * j),
+                             sw128_desc(a + 16384, BN, 0, 16 * j), idesc, j > 0);
+                mma_commit(&empty[s]);
+                mma_commit(&acc_full[buf]);
+            }
+            if (*(volatile int*)&gave_up) {
+                mma_commit(&drained);
+                mbar_wait(&drained, 0);
+            }
+        }
+    } else {
+#pragma unroll
+        for (int m = 0; m < BN; ++m) acc[m] = 0.f;
+        float* factors = reinterpret_cast<float*>(smem + Lay::kFactors) + warp * 2 * BN;
+        constexpr int kPer = (BN + 31) / 32;
+        float next[kPer];
+        const float* swp = sw + (int64_t)tile * groups;
+        const auto fetch = [&](int g) {
+            const float w = __ldg(swp + g);
+#pragma unroll
+            for (int p = 0; p < kPer; ++p) {
+                const int m = m0 + p * 32 + lane;
+                next[p] = (BN >= 32 || lane < BN) && m < M ? __ldg(sx + (int64_t)m * groups + g) * w : 0.f;
+            }
+        };
+        if (count > 0) fetch(g0);
+        for (int i = 0; i < count; ++i) {
+            const int buf = i & 1;
+            float* f = factors + buf * BN;
+#pragma unroll
+            for (int p = 0; p < kPer; ++p)
+                if (BN >= 32 || lane < BN) f[p * 32 + lane] = next[p];
+            if (i + 1 < count) fetch(g0 + i + 1);
+            __syncwarp();
+            if (!wait_or_give_up(&acc_full[buf], (i >> 1) & 1, &gave_up)) break;
+            tc_fence_after_sync();
+#pragma unroll
+            for (int c = 0; c < BN; c += 16) {
+                float d[16];
+                tmem_ld16(tmem + ((uint32_t)(warp * 32) << 16) + buf * BN + c, d);
+                tmem_ld_wait_for(d);
+#pragma unroll
+                for (int q = 0; q < 16; q += 4) {
+                    const float4 w = *reinterpret_cast<const float4*>(f + c + q);
+                    acc[c + q] = fmaf(d[q], w.x, acc[c + q]);
+                    acc[c + q + 1] = fmaf(d[q + 1], w.y, acc[c + q + 1]);
+                    acc[c + q + 2] = fmaf(d[q + 2], w.z, acc[c + q + 2]);
+                    acc[c + q + 3] = fmaf(d[q + 3], w.w, acc[c + q + 3]);
+                }
+            }
+            tc_fence_before_sync();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&acc_empty[buf]);
+        }
+    }
+
+    const int tokens = M - m0 < BN ? M - m0 : BN;
+    if (split == 1) {
+        if (warp < 4) {
+            const OutColumn o(out, n0 + threadIdx.x);
+            if (o.pitch)
+#pragma unroll
+                for (int m = 0; m < BN; ++m)
+                    if (m < tokens) o.store(m0 + m, acc[m]);
+        }
+        __syncthreads();
+        if (warp == 5) tmem_dealloc(tmem, Lay::kTmemCols);
+        return;
+    }
+    // This CTA's part, [token][column], where the stages were: every MMA that
+    // read them has completed.
+    __syncthreads();
+    float* parts = reinterpret_cast<float*>(smem);
+    if (warp < 4) {
+#pragma unroll
+        for (int m = 0; m < BN; ++m)
+            if (m < tokens) parts[m * 128 + threadIdx.x] = acc[m];
+    }
+    // TMEM is given back before the CTA waits for its peers
+    if (warp == 5) tmem_dealloc(tmem, Lay::kTmemCols);
+    __syncwarp();
+    cluster_sync();
+    if (warp < 4) {
+        const OutColumn o(out, n0 + threadIdx.x);
+        for (int m = part; m < tokens; m += split) {
+            const uint32_t at = smem_u32(parts + m * 128 + threadIdx.x);
+            float v = 0.f;
+            for (int r = 0; r < split; ++r) v += ld_cluster(at, r);
+            if (o.pitch) o.store(m0 + m, v);
+        }
+    }
+    __syncwarp();
+    cluster_sync();
+}
+
+using EncodeTiledFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*,
+                                   const cuuint64_t*, const cuuint64_t*, const cuuint32_t*,
+                                   const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
+                                   CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+// The driver's tensor-map encoder, fetched through the runtime once.
+cudaError_t tensor_map_encoder(EncodeTiledFn* fn) {
+    static EncodeTiledFn cached = nullptr;
+    if (!cached) {
+        void* p = nullptr;
+        cudaDriverEntryPointQueryResult q = cudaDriverEntryPointSymbolNotFound;
+        const cudaError_t e = cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &p, cudaEnableDefault, &q);
+        if (e != cudaSuccess) return e;
+        if (q != cudaDriverEntryPointSuccess || p == nullptr) return cudaErrorSymbolNotFound;
+        cached = reinterpret_cast<EncodeTiledFn>(p);
+    }
+    *fn = cached;
+    return cudaSuccess;
+}
+
+// Map of [rows][k] codes, box `box_rows` rows x 128 codes, 128-byte swizzle;
+// rows and codes past the tensor's ends read as zero.
+cudaError_t codes_map(EncodeTiledFn enc, CUtensorMap* m, const void* base, int64_t rows, int k, int box_rows) {
+    const cuuint64_t dims[2] = {(cuuint64_t)k, (cuuint64_t)rows};
+    const cuuint64_t strides[1] = {(cuuint64_t)k};
+    const cuuint32_t box[2] = {(cuuint32_t)kFp8Group, (cuuint32_t)box_rows};
+    const cuuint32_t estr[2] = {1u, 1u};
+    const CUresult r = enc(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(base), dims, strides, box,
+                           estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                           CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
+}
+
+// Launch with the cluster size and programmatic stream serialization.
+template <typename... KArgs, typename... Args>
+cudaError_t launch_cluster(void (*kern)(KArgs...), dim3 grid, dim3 block, size_t smem, int cluster,
+                           cudaStream_t st, Args&&... args) {
+    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (e != cudaSuccess) return e;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = (unsigned)cluster;
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = block;
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = st;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    return cudaLaunchKernelEx(&cfg, kern, std::forward<Args>(args)...);
+}
+
+OutRanges out_ranges(const gdr_linear_fp8_args& a) {
+    OutRanges o{};
+    o.n_outs = a.n_outs;
+    for (int i = 0; i < a.n_outs; ++i) {
+        o.begin[i + 1] = o.begin[i] + a.out_cols[i];
+        o.f32[i] = a.out_dtype[i] == GDR_F32;
+        o.ptr[i] = a.out[i];
+    }
+    return o;
+}
+
+template <int BN>
+cudaError_t launch_few(const gdr_linear_fp8_args& a, EncodeTiledFn enc, cudaStream_t st) {
+    const int groups = fp8_groups(a.k), tiles = fp8_groups(a.n);
+    const int64_t token_tiles = (a.rows + BN - 1) / BN;
+    if (token_tiles > 65535) return cudaErrorInvalidValue;
+    // as many parts of K as fill the SMs twice, none without work
+    int64_t split = 2 * 148 / (tiles * token_tiles);
+    split = split < 1 ? 1 : split > 8 ? 8 : split;
+    if (split > groups) split = groups;
+    if (tiles * split > (int64_t)INT32_MAX) return cudaErrorInvalidValue;
+    CUtensorMap mw, mx;
+    cudaError_t e;
+    if ((e = codes_map(enc, &mw, a.w, a.n, a.k, 128)) != cudaSuccess) return e;
+    if ((e = codes_map(enc, &mx, a.x, a.rows, a.k, BN)) != cudaSuccess) return e;
+    return launch_cluster(linear_few_kernel<BN>, dim3((unsigned)(tiles * split), (unsigned)token_tiles),
+                          dim3(kFewThreads), FewLayout<BN>::kDynBytes, (int)split, st, mw, mx, a.x_scale,
+                          a.w_scale, (int)a.rows, groups, (int)split, out_ranges(a));
+}
+
+}  // namespace
+
+cudaError_t launch_linear_fp8(const gdr_linear_fp8_args& a, cudaStream_t st) {
+    EncodeTiledFn enc = nullptr;
+    cudaError_t e = tensor_map_encoder(&enc);
+    if (e != cudaSuccess) return e;
+    if (a.rows <= 16) return launch_few<16>(a, enc, st);
+    if (a.rows <= 32) return launch_few<32>(a, enc, st);
+    if (a.rows <= 64) return launch_few<64>(a, enc, st);
+    return launch_few<128>(a, enc, st);
+}
+
+}  // namespace gdr
+
+extern "C" gdr_status gdr_linear_fp8_status(void* stream) {
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    cudaStreamCaptureStatus cs = cudaStreamCaptureStatusNone;
+    if (cudaStreamIsCapturing(st, &cs) != cudaSuccess || cs != cudaStreamCaptureStatusNone) {
+        (void)cudaGetLastError();
+        return GDR_ERR_CUDA;
+    }
+    uint32_t word = 0, zero = 0;
+    if (cudaMemcpyFromSymbolAsync(&word, gdr::g_linear_error, sizeof(word), 0, cudaMemcpyDeviceToHost, st) != cudaSuccess ||
+        cudaStreamSynchronize(st) != cudaSuccess) {
+        (void)cudaGetLastError();
+        return GDR_ERR_CUDA;
+    }
+    if (word == 0) return GDR_OK;
+    if (cudaMemcpyToSymbolAsync(gdr::g_linear_error, &zero, sizeof(zero), 0, cudaMemcpyHostToDevice, st) != cudaSuccess ||
+        cudaStreamSynchronize(st) != cudaSuccess) {
+        (void)cudaGetLastError();
+        return GDR_ERR_CUDA;
+    }
+    return GDR_ERR_TIMEOUT;
+}

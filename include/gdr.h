@@ -489,6 +489,140 @@ gdr_status gdr_decode_accept(int batch, int n_tokens, int n_heads, int d_k, int 
                              const int32_t* n_accept, const float* token_states, float* state,
                              void* stream);
 
+/* ------------------------------------------------------------------------
+ * 8-bit projections: what a mixer layer computes before its raw projections
+ * (RMSNorm of the residual stream, one matrix product) and after its outputs
+ * (gated per-head RMSNorm, one matrix product), with 8-bit operands ("kda-graft",
+ * section "Идея и архитектура": the graft keeps the layer's q, k, v and output
+ * projections and adds those of the decay and of the write strength).
+ *
+ * Format.  Codes are e4m3 (fp8 without infinities, largest value 448), one
+ * byte each, row-major.  A group is 128 consecutive channels of one row
+ * (activations) or a 128 x 128 block (weights); the last group of a row or
+ * column is shorter when the width is no multiple of 128.  Every group has one
+ * fp32 scale
+ *     s = max(max |y|, 1e-12) / 448
+ * and stands for the values s * code, with code = y / s rounded to the nearest
+ * e4m3 value (ties to even).  A group that holds a NaN has scale NaN and NaN
+ * codes; one that holds an infinity has an infinite scale, codes 0 for its
+ * finite values and NaN for the infinite ones.
+ *     activations  codes [rows, width], scales [rows, ceil(width / 128)]
+ *     weights      codes [N, K],        scales [ceil(N / 128), ceil(K / 128)]
+ * All sums and products before the rounding are fp32.
+ * ---------------------------------------------------------------------- */
+
+/* RMSNorm of the residual stream with the residual's addition:
+ *     h = x + residual                 (h = x without a residual)
+ *     y = h / sqrt(mean_c h_c^2 + norm_eps) * norm_weight
+ * The sum h stays fp32 for the norm; residual_out receives it rounded once to
+ * io_dtype. */
+#define GDR_NORM_MAX_WIDTH 32768
+typedef struct {
+    int64_t rows;               /* >= 0; at most INT32_MAX */
+    int width;                  /* channels per row: a multiple of 16, 16 .. GDR_NORM_MAX_WIDTH */
+    gdr_dtype io_dtype;         /* dtype of x, residual and residual_out */
+    const void* x;              /* device [rows, width] */
+    const void* residual;       /* device [rows, width], or NULL */
+    const float* norm_weight;   /* device [width] */
+    float norm_eps;             /* >= 0 */
+    void* residual_out;         /* device [rows, width] (output), or NULL: h is not kept.  May be
+                                   the same buffer as x or residual.  NULL without residual. */
+    void* y;                    /* device [rows, width] e4m3 codes (output) */
+    float* y_scale;             /* device [rows, ceil(width / 128)] (output) */
+} gdr_norm_fp8_args;
+
+/*
+ * Enqueue the norm.  x, residual, norm_weight, residual_out and y must be
+ * 16-byte aligned.  rows == 0 is a no-op.  Errors: GDR_ERR_INVALID_ARG (null or
+ * misaligned pointer, bad size or dtype, residual_out without residual,
+ * norm_eps negative or not finite), GDR_ERR_UNSUPPORTED (width no multiple of
+ * 16 or above GDR_NORM_MAX_WIDTH), GDR_ERR_CUDA on a failed launch.
+ */
+gdr_status gdr_norm_fp8(const gdr_norm_fp8_args* args, void* stream);
+
+/* The mixer's output epilogue (as gdr_prefill_args.gate_raw) with 8-bit codes
+ * as its result, from outputs that were computed without it: per token and head
+ *     y = o / sqrt(mean_c o_c^2 + norm_eps) * norm_weight * sigmoid(gate_raw)
+ * The codes' groups run over the token's H * d_v channels (at d_v 64 a group
+ * holds two heads).  o may be a prefill's (bf16 or fp32) or a decode step's
+ * (fp32) output. */
+typedef struct {
+    int64_t rows;               /* tokens >= 0; at most INT32_MAX */
+    int n_heads;                /* H >= 1 */
+    int d_v;                    /* 64 or 128 */
+    gdr_dtype o_dtype;          /* dtype of o */
+    gdr_dtype gate_dtype;       /* dtype of gate_raw */
+    const void* o;              /* device [rows, H, d_v] */
+    const void* gate_raw;       /* device [rows, H, d_v] */
+    const float* norm_weight;   /* device [d_v], shared by the heads */
+    float norm_eps;             /* >= 0 */
+    void* y;                    /* device [rows, H * d_v] e4m3 codes (output) */
+    float* y_scale;             /* device [rows, ceil(H * d_v / 128)] (output) */
+} gdr_gated_norm_fp8_args;
+
+/*
+ * Enqueue the gated norm.  o, gate_raw, norm_weight and y must be 16-byte
+ * aligned.  rows == 0 is a no-op.  Errors as for gdr_norm_fp8
+ * (GDR_ERR_UNSUPPORTED: d_v not 64 or 128; H * d_v above INT32_MAX is
+ * GDR_ERR_INVALID_ARG).
+ */
+gdr_status gdr_gated_norm_fp8(const gdr_gated_norm_fp8_args* args, void* stream);
+
+/*
+ * Weights as codes and block scales (once, when a model is loaded):
+ *   w        device [n, k], dtype w_dtype; row = output channel
+ *   codes    device [n, k] e4m3 (output)
+ *   scales   device [ceil(n / 128), ceil(k / 128)] (output)
+ * n >= 0 rows (0 is a no-op); k a multiple of 16 (else GDR_ERR_UNSUPPORTED),
+ * at least 16.  w and codes must be 16-byte aligned.
+ */
+gdr_status gdr_quantize_weight_fp8(int n, int k, gdr_dtype w_dtype, const void* w, void* codes,
+                                   float* scales, void* stream);
+
+/* Matrix product of 8-bit operands:
+ *     y[m, c] = sum_b x_scale[m, b] w_scale[c / 128, b] sum_{j in group b} x[m, j] w[c, j]
+ * The products of a group of 128 are summed by the tensor core in fp32, the
+ * groups in fp32 registers in order of b (where the sum is split over CTAs,
+ * the parts are added in order).  The result is rounded once to the output's
+ * dtype, and equal inputs give equal bits.
+ *
+ * The n output columns are cut into n_outs consecutive ranges, each written to
+ * a dense tensor of its own: one product over the stacked weights of several
+ * projections gives, for instance, x_q, x_k, x_v, a_raw and beta_raw in the
+ * layouts of gdr_preprocess and gdr_prefill_from_projections. */
+#define GDR_LINEAR_MAX_OUTS 8
+typedef struct {
+    int64_t rows;               /* M >= 0 tokens; at most INT32_MAX */
+    int n;                      /* N >= 1 output columns (rows of w) */
+    int k;                      /* K: a multiple of 16, at least 16 */
+    const void* x;              /* device [M, K] e4m3 codes */
+    const float* x_scale;       /* device [M, ceil(K / 128)] */
+    const void* w;              /* device [N, K] e4m3 codes */
+    const float* w_scale;       /* device [ceil(N / 128), ceil(K / 128)] */
+    int n_outs;                 /* 1 .. GDR_LINEAR_MAX_OUTS column ranges */
+    int out_cols[GDR_LINEAR_MAX_OUTS];         /* width of each range >= 1; they add up to N */
+    gdr_dtype out_dtype[GDR_LINEAR_MAX_OUTS];  /* dtype of each range's tensor */
+    void* out[GDR_LINEAR_MAX_OUTS];            /* device [M, out_cols[i]] (output) */
+} gdr_linear_fp8_args;
+
+/*
+ * Enqueue the product.  x and w must be 16-byte aligned; outputs need their
+ * element alignment and must not overlap each other or the inputs.  rows == 0
+ * is a no-op.  Errors: GDR_ERR_INVALID_ARG, GDR_ERR_UNSUPPORTED (K no multiple
+ * of 16), GDR_ERR_CUDA.
+ */
+gdr_status gdr_linear_fp8(const gdr_linear_fp8_args* args, void* stream);
+
+/*
+ * What the device side of the gdr_linear_fp8 calls on the current device since
+ * the last call of this function recorded: GDR_OK, or GDR_ERR_TIMEOUT if one
+ * of their kernels gave up a bounded wait (its outputs are then undefined); the
+ * record is cleared.  It is one word for all streams of the device.
+ * Synchronises `stream`, so it cannot be called while `stream` is capturing
+ * (GDR_ERR_CUDA).
+ */
+gdr_status gdr_linear_fp8_status(void* stream);
+
 #ifdef __cplusplus
 }
 #endif

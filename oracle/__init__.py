@@ -18,6 +18,8 @@ Contents
 * ``preprocess``: the mixer's input activations from raw projections -- the
   causal depthwise conv of width 4 on q, k, v, L2 norm of q and k, beta as a
   sigmoid and log a as a log-sigmoid of the biased gate (numpy, fp64).
+* ``norm_fp8`` / ``gated_norm_fp8`` / ``quantize_weight_fp8`` / ``linear_fp8``:
+  the 8-bit projections around the mixer (numpy, fp64).
 * ``chunk_factors`` / ``chunked_prefill``: the chunked form of the same
   recurrence written from its definition (numpy, fp64).  It is used to check
   the intermediate results of the intra-chunk kernel; it is itself pinned by
@@ -392,3 +394,75 @@ def output_epilogue(o, gate_raw, norm_weight, eps: float = 1e-6) -> np.ndarray:
     o = f64(o)
     ms = np.mean(o * o, axis=-1, keepdims=True)
     return o / np.sqrt(ms + eps) * f64(norm_weight) * sigmoid(f64(gate_raw))
+
+
+# ---------------------------------------------------------------------------
+# 8-bit projections (fp64): groups of 128 channels with one scale each,
+# scale = max(max |y|, 1e-12) / 448, codes e4m3.  The functions return what the
+# codes stand for before rounding ("y / scale"), so a test can ask how far a
+# stored code is from it; ``e4m3`` rounds.
+# ---------------------------------------------------------------------------
+FP8_GROUP = 128
+
+
+def e4m3(t) -> np.ndarray:
+    """Round to the nearest e4m3 value, ties to even: 3 mantissa bits, exponents
+    from -6 (below it, subnormals in steps of 2^-9), saturating at 448."""
+    t = f64(t)
+    a = np.minimum(np.abs(t), 448.0)
+    with np.errstate(divide="ignore"):
+        e = np.maximum(np.floor(np.log2(a)), -6.0)
+    step = np.exp2(e - 3)
+    return np.copysign(np.rint(a / step) * step, t)       # np.rint: ties to even
+
+
+def _scaled_rows(y):
+    """(y / scale, scale) of [rows, width] values, groups of 128 along a row."""
+    rows, width = y.shape
+    n = -(-width // FP8_GROUP)
+    scale = np.zeros((rows, n))
+    codes = np.zeros_like(y)
+    for j in range(n):
+        at = slice(FP8_GROUP * j, FP8_GROUP * (j + 1))
+        scale[:, j] = np.maximum(np.abs(y[:, at]).max(axis=1), 1e-12) / 448.0
+        codes[:, at] = y[:, at] / scale[:, j:j + 1]
+    return codes, scale
+
+
+def norm_fp8(x, norm_weight, residual=None, eps: float = 1e-6):
+    """h = x + residual; y = h / sqrt(mean h^2 + eps) * norm_weight; returns
+    (y / scale, scale, h)."""
+    h = f64(x) if residual is None else f64(x) + f64(residual)
+    y = h / np.sqrt(np.mean(h * h, axis=-1, keepdims=True) + eps) * f64(norm_weight)
+    return (*_scaled_rows(y), h)
+
+
+def gated_norm_fp8(o, gate_raw, norm_weight, eps: float = 1e-6):
+    """``output_epilogue`` with the token's H * d_v channels in groups of 128."""
+    y = output_epilogue(o, gate_raw, norm_weight, eps)
+    return _scaled_rows(y.reshape(y.shape[0], -1))
+
+
+def quantize_weight_fp8(w):
+    """(w / scale, scale) with one scale per 128 x 128 block."""
+    w = f64(w)
+    n, k = w.shape
+    bn, bk = -(-n // FP8_GROUP), -(-k // FP8_GROUP)
+    scale = np.zeros((bn, bk))
+    codes = np.zeros_like(w)
+    for i in range(bn):
+        for j in range(bk):
+            at = (slice(FP8_GROUP * i, FP8_GROUP * (i + 1)), slice(FP8_GROUP * j, FP8_GROUP * (j + 1)))
+            scale[i, j] = np.maximum(np.abs(w[at]).max(), 1e-12) / 448.0
+            codes[at] = w[at] / scale[i, j]
+    return codes, scale
+
+
+def linear_fp8(x, x_scale, w, w_scale):
+    """(y, sum |terms|): the product of the operands that the codes and scales
+    stand for, and the sum of its terms' sizes (what rounding errors scale with)."""
+    k, n = x.shape[1], w.shape[0]
+    a = f64(x) * np.repeat(f64(x_scale), FP8_GROUP, axis=1)[:, :k]
+    ws = np.repeat(np.repeat(f64(w_scale), FP8_GROUP, axis=0)[:n], FP8_GROUP, axis=1)[:, :k]
+    b = f64(w) * ws
+    return a @ b.T, np.abs(a) @ np.abs(b).T
