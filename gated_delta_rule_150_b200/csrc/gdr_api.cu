@@ -26,6 +26,8 @@ gdr_status from_cuda(cudaError_t e) {
 
 bool supported_width(int d) { return d == 64 || d == 128; }
 bool valid_dtype(gdr_dtype dt) { return dt == GDR_BF16 || dt == GDR_F32; }
+// Rows and columns of the 8-bit calls: kernels round them up to whole tiles in 32 bits.
+constexpr int64_t kMaxRows = (int64_t)INT32_MAX - 1023;
 bool valid_eps(float eps) { return eps >= 0.f && eps <= 3.0e38f; }
 
 // Shared checks of the prefill arguments that do not depend on outputs.
@@ -498,7 +500,7 @@ gdr_status gdr_decode_accept(int batch, int n_tokens, int n_heads, int d_k, int 
 
 gdr_status gdr_norm_fp8(const gdr_norm_fp8_args* a, void* stream) {
     if (!a) return GDR_ERR_INVALID_ARG;
-    if (a->rows < 0 || a->rows > (int64_t)INT32_MAX || a->width <= 0) return GDR_ERR_INVALID_ARG;
+    if (a->rows < 0 || a->rows > kMaxRows || a->width <= 0) return GDR_ERR_INVALID_ARG;
     if (!valid_dtype(a->io_dtype) || !valid_eps(a->norm_eps)) return GDR_ERR_INVALID_ARG;
     if (a->width % 16 != 0 || a->width > GDR_NORM_MAX_WIDTH) return GDR_ERR_UNSUPPORTED;
     if (a->residual_out && !a->residual) return GDR_ERR_INVALID_ARG;
@@ -513,12 +515,12 @@ gdr_status gdr_norm_fp8(const gdr_norm_fp8_args* a, void* stream) {
 
 gdr_status gdr_gated_norm_fp8(const gdr_gated_norm_fp8_args* a, void* stream) {
     if (!a) return GDR_ERR_INVALID_ARG;
-    if (a->rows < 0 || a->rows > (int64_t)INT32_MAX || a->n_heads <= 0 || a->d_v <= 0)
+    if (a->rows < 0 || a->rows > kMaxRows || a->n_heads <= 0 || a->d_v <= 0)
         return GDR_ERR_INVALID_ARG;
     if (!valid_dtype(a->o_dtype) || !valid_dtype(a->gate_dtype) || !valid_eps(a->norm_eps))
         return GDR_ERR_INVALID_ARG;
     if (!supported_width(a->d_v)) return GDR_ERR_UNSUPPORTED;
-    if ((int64_t)a->n_heads * a->d_v > (int64_t)INT32_MAX) return GDR_ERR_INVALID_ARG;
+    if ((int64_t)a->n_heads * a->d_v > kMaxRows) return GDR_ERR_INVALID_ARG;
     if (a->rows == 0) return GDR_OK;
     const void* v16[] = {a->o, a->gate_raw, a->norm_weight, a->y};
     for (const void* p : v16)
@@ -529,7 +531,7 @@ gdr_status gdr_gated_norm_fp8(const gdr_gated_norm_fp8_args* a, void* stream) {
 
 gdr_status gdr_quantize_weight_fp8(int n, int k, gdr_dtype w_dtype, const void* w, void* codes,
                                    float* scales, void* stream) {
-    if (n < 0 || k <= 0 || !valid_dtype(w_dtype)) return GDR_ERR_INVALID_ARG;
+    if (n < 0 || n > kMaxRows || k <= 0 || k > kMaxRows || !valid_dtype(w_dtype)) return GDR_ERR_INVALID_ARG;
     if (k % 16 != 0) return GDR_ERR_UNSUPPORTED;
     if (n == 0) return GDR_OK;
     if (!w || !aligned16(w) || !codes || !aligned16(codes) || !scales || !aligned4(scales))
@@ -540,7 +542,8 @@ gdr_status gdr_quantize_weight_fp8(int n, int k, gdr_dtype w_dtype, const void* 
 
 gdr_status gdr_linear_fp8(const gdr_linear_fp8_args* a, void* stream) {
     if (!a) return GDR_ERR_INVALID_ARG;
-    if (a->rows < 0 || a->rows > (int64_t)INT32_MAX || a->n <= 0 || a->k <= 0)
+    if (a->rows < 0 || a->rows > kMaxRows || a->n <= 0 || a->n > kMaxRows ||
+        a->k <= 0 || a->k > kMaxRows)
         return GDR_ERR_INVALID_ARG;
     if (a->k % 16 != 0) return GDR_ERR_UNSUPPORTED;
     if (a->n_outs < 1 || a->n_outs > GDR_LINEAR_MAX_OUTS) return GDR_ERR_INVALID_ARG;

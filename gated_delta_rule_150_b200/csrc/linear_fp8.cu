@@ -72,16 +72,17 @@ __device__ __forceinline__ void mbar_arrive(uint64_t* bar) {
     asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_u32(bar)) : "memory");
 }
 
-__device__ __forceinline__ void cluster_sync() {
-    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+// 32 bytes (a whole sector) in one store; p is 32-byte aligned.
+__device__ __forceinline__ void st_global_32(void* p, uint32_t a, uint32_t b, uint32_t c, uint32_t d,
+                                             uint32_t e, uint32_t f, uint32_t g, uint32_t h) {
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};"
+                 ::"l"(p), "r"(a), "r"(b), "r"(c), "r"(d), "r"(e), "r"(f), "r"(g), "r"(h) : "memory");
 }
 
 // Read a float of CTA `rank` of the cluster at the place `addr` of this CTA.
 __device__ __forceinline__ float ld_cluster(uint32_t addr, uint32_t rank) {
-    uint32_t at;
     float v;
-    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"(addr), "r"(rank));
-    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(at) : "memory");
+    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(cluster_addr(addr, rank)) : "memory");
     return v;
 }
 
@@ -204,7 +205,8 @@ linear_few_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_consta
                 if (BN >= 32 || lane < BN) f[p * 32 + lane] = next[p];
             if (i + 1 < count) fetch(g0 + i + 1);
             __syncwarp();
-            if (!wait_or_give_up(&acc_full[buf], (i >> 1) & 1, &gave_up)) break;
+            // the whole warp goes on or none of it (TMEM loads are warp-wide)
+            if (!__all_sync(0xffffffffu, wait_or_give_up(&acc_full[buf], (i >> 1) & 1, &gave_up))) break;
             tc_fence_after_sync();
 #pragma unroll
             for (int c = 0; c < BN; c += 16) {
@@ -261,6 +263,219 @@ linear_few_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_consta
             if (o.pitch) o.store(m0 + m, v);
         }
     }
+    __syncwarp();
+    cluster_sync();
+}
+
+// ---------------------------------------------------------------------------
+// Many tokens: CTA pairs on tiles of 256 tokens x 256 columns.  Each CTA loads
+// 128 tokens and 128 columns per K group (32 KB for 512 cycles of MMA, half of
+// what single CTAs on 128 x 256 tiles would pull through L2), holds its 128
+// tokens x 256 columns in two TMEM accumulators, and adds each finished group
+// into registers with its factor:
+//   warps 0-7   a thread owns a token (row) and 128 columns: one weight block,
+//               so a group's factor sx sw is one number per thread
+//   warp 8      TMA loads (one lane)
+//   warp 9      TMEM allocation; in the even CTA the MMAs (one lane)
+// Persistent: a pair takes tiles a grid stride apart, and the loads and MMAs of
+// the next tile run while the outputs of the last one are stored.
+// ---------------------------------------------------------------------------
+constexpr int kPairThreads = 320;
+constexpr int kPairStages = 6;
+constexpr uint32_t kPairStageBytes = 32768u;                 // 128 tokens + 128 columns of codes
+constexpr uint32_t kPairStagePitch = 33;                     // floats per staged output row (no bank conflicts)
+constexpr uint32_t kPairStaging = kPairStages * kPairStageBytes;
+constexpr uint32_t kPairBytes = kPairStaging + 8u * 32u * kPairStagePitch * 4u;
+constexpr uint32_t kPairDynBytes = kPairBytes + 1024u;
+constexpr int kPairRowGroup = 8;                             // token tiles that take their column tiles together
+
+// Tile t of a tile grid: bands of kPairRowGroup token tiles, column by column,
+// so that the tiles in flight share few rows of x and of w in L2.
+__device__ __forceinline__ void pair_tile(int t, int tiles_m, int tiles_n, int* tm, int* tn) {
+    const int band = t / (kPairRowGroup * tiles_n);
+    const int first = band * kPairRowGroup;
+    const int rows = tiles_m - first < kPairRowGroup ? tiles_m - first : kPairRowGroup;
+    const int r = t - first * tiles_n;
+    *tn = r / rows;
+    *tm = first + (r - *tn * rows);
+}
+
+__global__ void __launch_bounds__(kPairThreads, 1)
+linear_pair_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUtensorMap map_x,
+                   const float* __restrict__ sx, const float* __restrict__ sw, int M, int N, int groups,
+                   int tiles_m, int tiles_n, const __grid_constant__ OutRanges out) {
+    constexpr int ST = kPairStages;
+    extern __shared__ uint8_t dyn[];
+    uint8_t* smem = align_smem<1024>(dyn);
+    __shared__ uint64_t full[ST], empty[ST], acc_full[2], acc_empty[2], drained;
+    __shared__ uint32_t tmem_slot;
+    __shared__ int gave_up;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const uint32_t rank = cluster_rank();
+    const int pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
+    const int tiles = tiles_m * tiles_n;
+
+    if (threadIdx.x == 0) {
+        // full: the even CTA's, one arrival (its producer) and both CTAs' bytes;
+        // acc_empty: the even CTA's, eight warps of each CTA
+        for (int i = 0; i < ST; ++i) { mbar_init(&full[i], 1); mbar_init(&empty[i], 1); }
+        for (int i = 0; i < 2; ++i) { mbar_init(&acc_full[i], 1); mbar_init(&acc_empty[i], 16); }
+        mbar_init(&drained, 1);
+        gave_up = 0;
+        fence_mbar_init();
+    }
+    __syncwarp();
+    cluster_sync();
+    if (warp == 9) tmem_alloc_pair(&tmem_slot, 512);
+    tc_fence_before_sync();
+    __syncthreads();
+    tc_fence_after_sync();
+    const uint32_t tmem = tmem_slot;
+    pdl_wait();
+    pdl_launch_dependents();
+
+    if (warp == 8) {
+        if (lane == 0) {
+            int i = 0;
+            bool ok = true;
+            for (int t = pair; t < tiles && ok; t += pairs) {
+                int tm, tn;
+                pair_tile(t, tiles_m, tiles_n, &tm, &tn);
+                const int m0 = tm * 256 + (int)rank * 128, n0 = tn * 256 + (int)rank * 128;
+                for (int g = 0; g < groups; ++g, ++i) {
+                    const int s = i % ST;
+                    if (i >= ST && !wait_or_give_up(&empty[s], ((i / ST) & 1) ^ 1, &gave_up)) { ok = false; break; }
+                    if (rank == 0) mbar_arrive_expect_tx(&full[s], 2 * kPairStageBytes);
+                    const uint32_t bar = cluster_addr(smem_u32(&full[s]), 0);
+                    uint8_t* st = smem + s * kPairStageBytes;
+                    tma_load_2d_pair(st, &map_x, g * kFp8Group, m0, bar);
+                    tma_load_2d_pair(st + 16384, &map_w, g * kFp8Group, n0, bar);
+                }
+            }
+            // the last stages' releases must have landed before this CTA's shared
+            // memory goes; after a give-up, so must its copies (they are counted
+            // on the even CTA's barriers)
+            for (int j = i < ST ? 0 : i - ST; j < i; ++j)
+                if (!(*(volatile int*)&gave_up)) wait_or_give_up(&empty[j % ST], (j / ST) & 1, &gave_up);
+            if (*(volatile int*)&gave_up && rank == 0)
+                for (int j = i < ST ? 0 : i - ST; j < i; ++j) mbar_wait(&full[j % ST], (j / ST) & 1);
+        }
+    } else if (warp == 9) {
+        if (rank == 0 && lane == 0) {
+            constexpr uint32_t idesc = idesc_e4m3_f32(256, 256);
+            int i = 0;
+            bool ok = true;
+            for (int t = pair; t < tiles && ok; t += pairs) {
+                for (int g = 0; g < groups; ++g, ++i) {
+                    const int s = i % ST, buf = i & 1;
+                    if ((i >= 2 && !wait_or_give_up(&acc_empty[buf], ((i >> 1) & 1) ^ 1, &gave_up)) ||
+                        !wait_or_give_up(&full[s], (i / ST) & 1, &gave_up)) { ok = false; break; }
+                    tc_fence_after_sync();
+                    const uint32_t a = smem_u32(smem + s * kPairStageBytes);
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
+                        mma_e4m3_pair(tmem + buf * 256, sw128_desc(a, 128, 0, 16 * j),
+                                      sw128_desc(a + 16384, 128, 0, 16 * j), idesc, j > 0);
+                    mma_commit_pair(&empty[s]);
+                    mma_commit_pair(&acc_full[buf]);
+                }
+            }
+            if (*(volatile int*)&gave_up) {
+                mma_commit_pair(&drained);
+                mbar_wait(&drained, 0);
+            }
+        }
+    } else {
+        const int half = warp >> 2;                          // columns half * 128 .. + 127 of the tile
+        const uint32_t lane0 = (uint32_t)((warp & 3) * 32) << 16;
+        float* stage = reinterpret_cast<float*>(smem + kPairStaging) + warp * 32 * kPairStagePitch;
+        const uint32_t bar0 = cluster_addr(smem_u32(&acc_empty[0]), 0);
+        const uint32_t bar1 = cluster_addr(smem_u32(&acc_empty[1]), 0);
+        int i = 0;
+        bool ok = true;
+        for (int t = pair; t < tiles && ok; t += pairs) {
+            int tm, tn;
+            pair_tile(t, tiles_m, tiles_n, &tm, &tn);
+            const int row0 = tm * 256 + (int)rank * 128 + (warp & 3) * 32;
+            const int m = row0 + lane;
+            const int c0 = tn * 256 + half * 128;
+            const float* sxp = sx + (int64_t)(m < M ? m : 0) * groups;
+            const float* swp = sw + (int64_t)(c0 < N ? tn * 2 + half : 0) * groups;
+            float2 acc[64];
+#pragma unroll
+            for (int c = 0; c < 64; ++c) acc[c] = make_float2(0.f, 0.f);
+            float next = __ldg(sxp) * __ldg(swp);
+            for (int g = 0; g < groups; ++g, ++i) {
+                const int buf = i & 1;
+                const float f = next;
+                if (g + 1 < groups) next = __ldg(sxp + g + 1) * __ldg(swp + g + 1);
+                // the whole warp goes on or none of it (TMEM loads are warp-wide)
+                if (!__all_sync(0xffffffffu, wait_or_give_up(&acc_full[buf], (i >> 1) & 1, &gave_up))) { ok = false; break; }
+                tc_fence_after_sync();
+                const uint32_t at = tmem + lane0 + buf * 256 + half * 128;
+                const float2 ff = make_float2(f, f);
+                float d[2][16];
+                tmem_ld16(at, d[0]);
+#pragma unroll
+                for (int c = 0; c < 8; ++c) {
+                    tmem_ld_wait_for(d[c & 1]);
+                    if (c < 7) tmem_ld16(at + 16 * (c + 1), d[(c + 1) & 1]);
+#pragma unroll
+                    for (int q = 0; q < 8; ++q)
+                        acc[c * 8 + q] = __ffma2_rn(make_float2(d[c & 1][2 * q], d[c & 1][2 * q + 1]), ff, acc[c * 8 + q]);
+                }
+                tc_fence_before_sync();
+                __syncwarp();
+                if (lane == 0) mbar_arrive_cluster(buf ? bar1 : bar0);
+            }
+            if (!ok || c0 >= N) continue;
+            // Outputs: 128 columns inside one range, with rows that start on 32
+            // bytes, are stored by their threads (full 32-byte sectors); others go
+            // through shared memory, a lane per column.
+            int r = 0;
+            while (r + 1 < out.n_outs && c0 >= out.begin[r + 1]) ++r;
+            const int pitch = out.begin[r + 1] - out.begin[r], off = c0 - out.begin[r];
+            const int elem = out.f32[r] ? 4 : 2;
+            const bool direct = c0 + 128 <= out.begin[r + 1] && (pitch * elem) % 32 == 0 && (off * elem) % 32 == 0 &&
+                                (reinterpret_cast<uint64_t>(out.ptr[r]) & 31u) == 0;
+            if (direct) {
+                if (m < M) {
+                    uint8_t* p = (uint8_t*)out.ptr[r] + ((int64_t)m * pitch + off) * elem;
+                    if (elem == 4) {
+#pragma unroll
+                        for (int c = 0; c < 64; c += 4) st_global_32(p + c * 8, __float_as_uint(acc[c].x), __float_as_uint(acc[c].y),
+                            __float_as_uint(acc[c + 1].x), __float_as_uint(acc[c + 1].y), __float_as_uint(acc[c + 2].x),
+                            __float_as_uint(acc[c + 2].y), __float_as_uint(acc[c + 3].x), __float_as_uint(acc[c + 3].y));
+                    } else {
+#pragma unroll
+                        for (int c = 0; c < 64; c += 8) st_global_32(p + c * 4, pack_bf16(acc[c].x, acc[c].y),
+                            pack_bf16(acc[c + 1].x, acc[c + 1].y), pack_bf16(acc[c + 2].x, acc[c + 2].y),
+                            pack_bf16(acc[c + 3].x, acc[c + 3].y), pack_bf16(acc[c + 4].x, acc[c + 4].y),
+                            pack_bf16(acc[c + 5].x, acc[c + 5].y), pack_bf16(acc[c + 6].x, acc[c + 6].y),
+                            pack_bf16(acc[c + 7].x, acc[c + 7].y));
+                    }
+                }
+                continue;
+            }
+            const int rows = M - row0 < 32 ? M - row0 : 32;
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                __syncwarp();
+#pragma unroll
+                for (int c = 0; c < 16; ++c) {
+                    stage[lane * kPairStagePitch + 2 * c] = acc[q * 16 + c].x;
+                    stage[lane * kPairStagePitch + 2 * c + 1] = acc[q * 16 + c].y;
+                }
+                __syncwarp();
+                const OutColumn o(out, c0 + q * 32 + lane);
+                if (o.pitch)
+                    for (int j = 0; j < rows; ++j) o.store(row0 + j, stage[j * kPairStagePitch + lane]);
+            }
+        }
+    }
+    __syncthreads();
+    cluster_sync();
+    if (warp == 9) tmem_dealloc_pair(tmem, 512);
     __syncwarp();
     cluster_sync();
 }
@@ -351,6 +566,20 @@ cudaError_t launch_few(const gdr_linear_fp8_args& a, EncodeTiledFn enc, cudaStre
                           a.w_scale, (int)a.rows, groups, (int)split, out_ranges(a));
 }
 
+cudaError_t launch_pair(const gdr_linear_fp8_args& a, EncodeTiledFn enc, cudaStream_t st) {
+    const int groups = fp8_groups(a.k);
+    const int64_t tiles_m = (a.rows + 255) / 256, tiles_n = ((int64_t)a.n + 255) / 256;
+    if (tiles_m * tiles_n > (int64_t)INT32_MAX - 1024) return cudaErrorInvalidValue;
+    CUtensorMap mw, mx;
+    cudaError_t e;
+    if ((e = codes_map(enc, &mw, a.w, a.n, a.k, 128)) != cudaSuccess) return e;
+    if ((e = codes_map(enc, &mx, a.x, a.rows, a.k, 128)) != cudaSuccess) return e;
+    const int64_t pairs = tiles_m * tiles_n < 74 ? tiles_m * tiles_n : 74;
+    return launch_cluster(linear_pair_kernel, dim3((unsigned)(2 * pairs)), dim3(kPairThreads), kPairDynBytes, 2, st,
+                          mw, mx, a.x_scale, a.w_scale, (int)a.rows, a.n, groups, (int)tiles_m, (int)tiles_n,
+                          out_ranges(a));
+}
+
 }  // namespace
 
 cudaError_t launch_linear_fp8(const gdr_linear_fp8_args& a, cudaStream_t st) {
@@ -360,7 +589,8 @@ cudaError_t launch_linear_fp8(const gdr_linear_fp8_args& a, cudaStream_t st) {
     if (a.rows <= 16) return launch_few<16>(a, enc, st);
     if (a.rows <= 32) return launch_few<32>(a, enc, st);
     if (a.rows <= 64) return launch_few<64>(a, enc, st);
-    return launch_few<128>(a, enc, st);
+    if (a.rows <= 512) return launch_few<128>(a, enc, st);
+    return launch_pair(a, enc, st);
 }
 
 }  // namespace gdr

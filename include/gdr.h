@@ -508,7 +508,8 @@ gdr_status gdr_decode_accept(int batch, int n_tokens, int n_heads, int d_k, int 
  * finite values and NaN for the infinite ones.
  *     activations  codes [rows, width], scales [rows, ceil(width / 128)]
  *     weights      codes [N, K],        scales [ceil(N / 128), ceil(K / 128)]
- * All sums and products before the rounding are fp32.
+ * All sums and products before the rounding are fp32.  Rows, widths, N and K
+ * are at most 2^31 - 1024 (GDR_ERR_INVALID_ARG above).
  * ---------------------------------------------------------------------- */
 
 /* RMSNorm of the residual stream with the residual's addition:
@@ -518,7 +519,7 @@ gdr_status gdr_decode_accept(int batch, int n_tokens, int n_heads, int d_k, int 
  * io_dtype. */
 #define GDR_NORM_MAX_WIDTH 32768
 typedef struct {
-    int64_t rows;               /* >= 0; at most INT32_MAX */
+    int64_t rows;               /* >= 0 */
     int width;                  /* channels per row: a multiple of 16, 16 .. GDR_NORM_MAX_WIDTH */
     gdr_dtype io_dtype;         /* dtype of x, residual and residual_out */
     const void* x;              /* device [rows, width] */
@@ -547,7 +548,7 @@ gdr_status gdr_norm_fp8(const gdr_norm_fp8_args* args, void* stream);
  * holds two heads).  o may be a prefill's (bf16 or fp32) or a decode step's
  * (fp32) output. */
 typedef struct {
-    int64_t rows;               /* tokens >= 0; at most INT32_MAX */
+    int64_t rows;               /* tokens >= 0 */
     int n_heads;                /* H >= 1 */
     int d_v;                    /* 64 or 128 */
     gdr_dtype o_dtype;          /* dtype of o */
@@ -563,8 +564,8 @@ typedef struct {
 /*
  * Enqueue the gated norm.  o, gate_raw, norm_weight and y must be 16-byte
  * aligned.  rows == 0 is a no-op.  Errors as for gdr_norm_fp8
- * (GDR_ERR_UNSUPPORTED: d_v not 64 or 128; H * d_v above INT32_MAX is
- * GDR_ERR_INVALID_ARG).
+ * (GDR_ERR_UNSUPPORTED: d_v not 64 or 128; the limit above
+ * holds for H * d_v).
  */
 gdr_status gdr_gated_norm_fp8(const gdr_gated_norm_fp8_args* args, void* stream);
 
@@ -592,7 +593,7 @@ gdr_status gdr_quantize_weight_fp8(int n, int k, gdr_dtype w_dtype, const void* 
  * layouts of gdr_preprocess and gdr_prefill_from_projections. */
 #define GDR_LINEAR_MAX_OUTS 8
 typedef struct {
-    int64_t rows;               /* M >= 0 tokens; at most INT32_MAX */
+    int64_t rows;               /* M >= 0 tokens */
     int n;                      /* N >= 1 output columns (rows of w) */
     int k;                      /* K: a multiple of 16, at least 16 */
     const void* x;              /* device [M, K] e4m3 codes */
