@@ -55,17 +55,24 @@ struct OutColumn {
 // the CTA gave up or the limit ran out (then the error word is set).
 __device__ __forceinline__ bool wait_or_give_up(uint64_t* bar, uint32_t parity, volatile int* gave_up) {
     const uint32_t a = smem_u32(bar);
-    if (mbar_try_wait(a, parity)) return true;
-    const uint64_t t0 = global_timer_ns();
+    uint64_t t0 = 0;
     while (true) {
-        if (mbar_try_wait(a, parity)) return true;
+        for (int i = 0; i < 64; ++i)
+            if (mbar_try_wait(a, parity)) return true;
         if (*gave_up) return false;
+        if (t0 == 0) t0 = global_timer_ns();
         if (global_timer_ns() - t0 > kWaitLimitNs) {
             *gave_up = 1;
             atomicOr(&g_linear_error, 1u);
             return false;
         }
     }
+}
+
+// The same by a whole warp: every lane goes on or none does (what follows is
+// warp-wide: TMEM loads, elected issue).
+__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volatile int* gave_up) {
+    return __all_sync(0xffffffffu, wait_or_give_up(bar, parity, gave_up));
 }
 
 __device__ __forceinline__ void mbar_arrive(uint64_t* bar) {
@@ -145,29 +152,29 @@ linear_few_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_consta
 
     float acc[BN];
     if (warp == 4) {
-        if (lane == 0) {
-            int issued = 0;
-            for (; issued < count; ++issued) {
-                const int s = issued % ST;
-                if (issued >= ST && !wait_or_give_up(&empty[s], ((issued / ST) & 1) ^ 1, &gave_up)) break;
+        int i = 0;
+        for (int s = 0, phase = 1; i < count; ++i) {
+            if (i >= ST && !warp_wait(&empty[s], phase, &gave_up)) break;
+            if (elect_one()) {
                 uint8_t* st = smem + s * Lay::kStageBytes;
                 mbar_arrive_expect_tx(&full[s], Lay::kStageBytes);
-                tma_load_2d(st, &map_w, (g0 + issued) * kFp8Group, n0, &full[s]);
-                tma_load_2d(st + 16384, &map_x, (g0 + issued) * kFp8Group, m0, &full[s]);
+                tma_load_2d(st, &map_w, (g0 + i) * kFp8Group, n0, &full[s]);
+                tma_load_2d(st + 16384, &map_x, (g0 + i) * kFp8Group, m0, &full[s]);
             }
-            // gave up: no copy may still be in flight when the CTA ends
-            if (*(volatile int*)&gave_up)
-                for (int i = issued < ST ? 0 : issued - ST; i < issued; ++i)
-                    mbar_wait(&full[i % ST], (i / ST) & 1);
+            __syncwarp();
+            if (++s == ST) { s = 0; phase ^= 1; }
         }
+        // gave up: no copy may still be in flight when the CTA ends
+        if (*(volatile int*)&gave_up)
+            for (int j = i < ST ? 0 : i - ST; j < i; ++j) mbar_wait(&full[j % ST], (j / ST) & 1);
     } else if (warp == 5) {
-        if (lane == 0) {
-            constexpr uint32_t idesc = idesc_e4m3_f32(128, BN);
-            for (int i = 0; i < count; ++i) {
-                const int s = i % ST, buf = i & 1;
-                if (i >= 2 && !wait_or_give_up(&acc_empty[buf], ((i >> 1) & 1) ^ 1, &gave_up)) break;
-                if (!wait_or_give_up(&full[s], (i / ST) & 1, &gave_up)) break;
-                tc_fence_after_sync();
+        constexpr uint32_t idesc = idesc_e4m3_f32(128, BN);
+        for (int i = 0, s = 0, phase = 0; i < count; ++i) {
+            const int buf = i & 1;
+            if (i >= 2 && !warp_wait(&acc_empty[buf], ((i >> 1) & 1) ^ 1, &gave_up)) break;
+            if (!warp_wait(&full[s], phase, &gave_up)) break;
+            tc_fence_after_sync();
+            if (elect_one()) {
                 const uint32_t a = smem_u32(smem + s * Lay::kStageBytes);
 #pragma unroll
                 for (int j = 0; j < 4; ++j)      // 32 codes = 32 bytes = 16 of the descriptor's 2-byte columns
@@ -176,10 +183,12 @@ linear_few_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_consta
                 mma_commit(&empty[s]);
                 mma_commit(&acc_full[buf]);
             }
-            if (*(volatile int*)&gave_up) {
-                mma_commit(&drained);
-                mbar_wait(&drained, 0);
-            }
+            __syncwarp();
+            if (++s == ST) { s = 0; phase ^= 1; }
+        }
+        if (*(volatile int*)&gave_up) {
+            if (lane == 0) mma_commit(&drained);
+            mbar_wait(&drained, 0);
         }
     } else {
 #pragma unroll
@@ -205,8 +214,7 @@ linear_few_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_consta
                 if (BN >= 32 || lane < BN) f[p * 32 + lane] = next[p];
             if (i + 1 < count) fetch(g0 + i + 1);
             __syncwarp();
-            // the whole warp goes on or none of it (TMEM loads are warp-wide)
-            if (!__all_sync(0xffffffffu, wait_or_give_up(&acc_full[buf], (i >> 1) & 1, &gave_up))) break;
+            if (!warp_wait(&acc_full[buf], (i >> 1) & 1, &gave_up)) break;
             tc_fence_after_sync();
 #pragma unroll
             for (int c = 0; c < BN; c += 16) {
@@ -335,53 +343,58 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_const
     pdl_launch_dependents();
 
     if (warp == 8) {
-        if (lane == 0) {
-            int i = 0;
-            bool ok = true;
-            for (int t = pair; t < tiles && ok; t += pairs) {
-                int tm, tn;
-                pair_tile(t, tiles_m, tiles_n, &tm, &tn);
-                const int m0 = tm * 256 + (int)rank * 128, n0 = tn * 256 + (int)rank * 128;
-                for (int g = 0; g < groups; ++g, ++i) {
-                    const int s = i % ST;
-                    if (i >= ST && !wait_or_give_up(&empty[s], ((i / ST) & 1) ^ 1, &gave_up)) { ok = false; break; }
+        int i = 0, s = 0, phase = 1;
+        bool ok = true;
+        for (int t = pair; t < tiles && ok; t += pairs) {
+            int tm, tn;
+            pair_tile(t, tiles_m, tiles_n, &tm, &tn);
+            const int m0 = tm * 256 + (int)rank * 128, n0 = tn * 256 + (int)rank * 128;
+            for (int g = 0; g < groups; ++g, ++i) {
+                if (i >= ST && !warp_wait(&empty[s], phase, &gave_up)) { ok = false; break; }
+                if (elect_one()) {
                     if (rank == 0) mbar_arrive_expect_tx(&full[s], 2 * kPairStageBytes);
                     const uint32_t bar = cluster_addr(smem_u32(&full[s]), 0);
                     uint8_t* st = smem + s * kPairStageBytes;
                     tma_load_2d_pair(st, &map_x, g * kFp8Group, m0, bar);
                     tma_load_2d_pair(st + 16384, &map_w, g * kFp8Group, n0, bar);
                 }
+                __syncwarp();
+                if (++s == ST) { s = 0; phase ^= 1; }
             }
-            // the last stages' releases must have landed before this CTA's shared
-            // memory goes; after a give-up, so must its copies (they are counted
-            // on the even CTA's barriers)
-            for (int j = i < ST ? 0 : i - ST; j < i; ++j)
-                if (!(*(volatile int*)&gave_up)) wait_or_give_up(&empty[j % ST], (j / ST) & 1, &gave_up);
-            if (*(volatile int*)&gave_up && rank == 0)
-                for (int j = i < ST ? 0 : i - ST; j < i; ++j) mbar_wait(&full[j % ST], (j / ST) & 1);
         }
+        // the last stages' releases must have landed before this CTA's shared
+        // memory goes; after a give-up, so must its copies (they are counted
+        // on the even CTA's barriers)
+        for (int j = i < ST ? 0 : i - ST; j < i; ++j)
+            if (!(*(volatile int*)&gave_up)) wait_or_give_up(&empty[j % ST], (j / ST) & 1, &gave_up);
+        if (*(volatile int*)&gave_up && rank == 0)
+            for (int j = i < ST ? 0 : i - ST; j < i; ++j) mbar_wait(&full[j % ST], (j / ST) & 1);
     } else if (warp == 9) {
-        if (rank == 0 && lane == 0) {
+        if (rank == 0) {
             constexpr uint32_t idesc = idesc_e4m3_f32(256, 256);
-            int i = 0;
+            int i = 0, s = 0, phase = 0;
             bool ok = true;
             for (int t = pair; t < tiles && ok; t += pairs) {
                 for (int g = 0; g < groups; ++g, ++i) {
-                    const int s = i % ST, buf = i & 1;
-                    if ((i >= 2 && !wait_or_give_up(&acc_empty[buf], ((i >> 1) & 1) ^ 1, &gave_up)) ||
-                        !wait_or_give_up(&full[s], (i / ST) & 1, &gave_up)) { ok = false; break; }
+                    const int buf = i & 1;
+                    if ((i >= 2 && !warp_wait(&acc_empty[buf], ((i >> 1) & 1) ^ 1, &gave_up)) ||
+                        !warp_wait(&full[s], phase, &gave_up)) { ok = false; break; }
                     tc_fence_after_sync();
-                    const uint32_t a = smem_u32(smem + s * kPairStageBytes);
+                    if (elect_one()) {
+                        const uint32_t a = smem_u32(smem + s * kPairStageBytes);
 #pragma unroll
-                    for (int j = 0; j < 4; ++j)
-                        mma_e4m3_pair(tmem + buf * 256, sw128_desc(a, 128, 0, 16 * j),
-                                      sw128_desc(a + 16384, 128, 0, 16 * j), idesc, j > 0);
-                    mma_commit_pair(&empty[s]);
-                    mma_commit_pair(&acc_full[buf]);
+                        for (int j = 0; j < 4; ++j)
+                            mma_e4m3_pair(tmem + buf * 256, sw128_desc(a, 128, 0, 16 * j),
+                                          sw128_desc(a + 16384, 128, 0, 16 * j), idesc, j > 0);
+                        mma_commit_pair(&empty[s]);
+                        mma_commit_pair(&acc_full[buf]);
+                    }
+                    __syncwarp();
+                    if (++s == ST) { s = 0; phase ^= 1; }
                 }
             }
             if (*(volatile int*)&gave_up) {
-                mma_commit_pair(&drained);
+                if (lane == 0) mma_commit_pair(&drained);
                 mbar_wait(&drained, 0);
             }
         }
@@ -409,8 +422,7 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_const
                 const int buf = i & 1;
                 const float f = next;
                 if (g + 1 < groups) next = __ldg(sxp + g + 1) * __ldg(swp + g + 1);
-                // the whole warp goes on or none of it (TMEM loads are warp-wide)
-                if (!__all_sync(0xffffffffu, wait_or_give_up(&acc_full[buf], (i >> 1) & 1, &gave_up))) { ok = false; break; }
+                if (!warp_wait(&acc_full[buf], (i >> 1) & 1, &gave_up)) { ok = false; break; }
                 tc_fence_after_sync();
                 const uint32_t at = tmem + lane0 + buf * 256 + half * 128;
                 const float2 ff = make_float2(f, f);

@@ -39,6 +39,17 @@ __device__ __forceinline__ uint64_t global_timer_ns() {
 // healthy chunk step takes (microseconds), far below a watchdog.
 constexpr uint64_t kWaitLimitNs = 2000000000ull;
 
+// True in one lane of a converged warp.  TMA and tcgen05 instructions take
+// their operands from uniform registers: issued by the elected lane of a warp
+// that runs its loop as a whole they cost a few cycles, under `lane == 0` the
+// compiler has to allow for any set of lanes (measured: a loop of one barrier
+// wait and two 16 KB tile loads took 972 cycles per turn that way, 534 so).
+__device__ __forceinline__ bool elect_one() {
+    uint32_t p;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
+    return p != 0;
+}
+
 // ---------------------------------------------------------------------------
 // mbarrier
 // ---------------------------------------------------------------------------
@@ -276,6 +287,16 @@ __device__ __forceinline__ void tmem_ld_wait_for(float (&r)[16]) {
                    "+f"(r[13]), "+f"(r[14]), "+f"(r[15]) :: "memory");
 }
 
+__device__ __forceinline__ void tmem_ld_wait_for(float (&r)[32]) {
+    asm volatile("tcgen05.wait::ld.sync.aligned;"
+                 : "+f"(r[0]), "+f"(r[1]), "+f"(r[2]), "+f"(r[3]), "+f"(r[4]), "+f"(r[5]), "+f"(r[6]),
+                   "+f"(r[7]), "+f"(r[8]), "+f"(r[9]), "+f"(r[10]), "+f"(r[11]), "+f"(r[12]),
+                   "+f"(r[13]), "+f"(r[14]), "+f"(r[15]), "+f"(r[16]), "+f"(r[17]), "+f"(r[18]),
+                   "+f"(r[19]), "+f"(r[20]), "+f"(r[21]), "+f"(r[22]), "+f"(r[23]), "+f"(r[24]),
+                   "+f"(r[25]), "+f"(r[26]), "+f"(r[27]), "+f"(r[28]), "+f"(r[29]), "+f"(r[30]),
+                   "+f"(r[31]) :: "memory");
+}
+
 // ---------------------------------------------------------------------------
 // tcgen05.mma, kind::f16 (bf16 x bf16 -> fp32 in TMEM), both operands in
 // shared memory, issued by a single thread.
@@ -346,8 +367,11 @@ __device__ __forceinline__ uint32_t cluster_addr(uint32_t addr, uint32_t rank) {
     return r;
 }
 
+// Arrive on a barrier of any CTA of the cluster.  Orders tensor-memory accesses
+// (with the tcgen05 fences) but no other memory across CTAs: release.cluster
+// would wait for a fence of several hundred cycles.
 __device__ __forceinline__ void mbar_arrive_cluster(uint32_t cluster_bar) {
-    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_bar) : "memory");
+    asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(cluster_bar) : "memory");
 }
 
 __device__ __forceinline__ void tmem_alloc_pair(uint32_t* slot, uint32_t ncols) {
