@@ -51,39 +51,25 @@ struct OutColumn {
     }
 };
 
-// A wait that ends: true once the phase completed, false when another role of
-// the CTA gave up or the limit ran out (then the error word is set).
-__device__ __forceinline__ bool wait_or_give_up(uint64_t* bar, uint32_t parity, volatile int* gave_up) {
-    const uint32_t a = smem_u32(bar);
-    uint64_t t0 = 0;
-    while (true) {
-        for (int i = 0; i < 64; ++i)
-            if (mbar_try_wait(a, parity)) return true;
-        if (*gave_up) return false;
-        if (t0 == 0) t0 = global_timer_ns();
-        if (global_timer_ns() - t0 > kWaitLimitNs) {
-            *gave_up = 1;
-            atomicOr(&g_linear_error, 1u);
-            return false;
-        }
-    }
-}
+// A whole warp's wait that ends: true once the phase completed, false when the
+// tries ran out (then the error word is set and the warp's role stops).  A try
+// suspends the warp for up to about a microsecond, so the limit is about a
+// second.  The loop is kept this small because it is on every role's critical
+// path: with a look at the timer in it the many-token kernel ran 10 to 30 %
+// slower.
+constexpr int kWaitTries = 1 << 20;
 
-// The same by a whole warp: every lane goes on or none does (what follows is
-// warp-wide: TMEM loads, elected issue).
-__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volatile int* gave_up) {
-    return __all_sync(0xffffffffu, wait_or_give_up(bar, parity, gave_up));
+__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, int* gave_up) {
+    const uint32_t a = smem_u32(bar);
+    for (int i = 0; i < kWaitTries; ++i)
+        if (__all_sync(0xffffffffu, mbar_try_wait(a, parity))) return true;
+    *gave_up = 1;
+    atomicOr(&g_linear_error, 1u);
+    return false;
 }
 
 __device__ __forceinline__ void mbar_arrive(uint64_t* bar) {
     asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_u32(bar)) : "memory");
-}
-
-// 32 bytes (a whole sector) in one store; p is 32-byte aligned.
-__device__ __forceinline__ void st_global_32(void* p, uint32_t a, uint32_t b, uint32_t c, uint32_t d,
-                                             uint32_t e, uint32_t f, uint32_t g, uint32_t h) {
-    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};"
-                 ::"l"(p), "r"(a), "r"(b), "r"(c), "r"(d), "r"(e), "r"(f), "r"(g), "r"(h) : "memory");
 }
 
 // Read a float of CTA `rank` of the cluster at the place `addr` of this CTA.
@@ -277,23 +263,28 @@ linear_few_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_consta
 
 // ---------------------------------------------------------------------------
 // Many tokens: CTA pairs on tiles of 256 tokens x 256 columns.  Each CTA loads
-// 128 tokens and 128 columns per K group (32 KB for 512 cycles of MMA, half of
-// what single CTAs on 128 x 256 tiles would pull through L2), holds its 128
-// tokens x 256 columns in two TMEM accumulators, and adds each finished group
-// into registers with its factor:
-//   warps 0-7   a thread owns a token (row) and 128 columns: one weight block,
-//               so a group's factor sx sw is one number per thread
-//   warp 8      TMA loads (one lane)
-//   warp 9      TMEM allocation; in the even CTA the MMAs (one lane)
-// Persistent: a pair takes tiles a grid stride apart, and the loads and MMAs of
-// the next tile run while the outputs of the last one are stored.
+// 128 tokens and 128 columns per K group (32 KB; two single CTAs on 128 x 256
+// tiles would pull 96 KB through L2), holds its 128 tokens x 256 columns in TMEM,
+// twice, and adds each finished group into registers with its factor.
+//   warps 0-7   a thread owns a token (row) and one half of the tile's columns,
+//               which is one weight block: a group's factor sx sw is one number
+//               per thread
+//   warp 8      TMA loads
+//   warps 9, 10 (even CTA) the MMAs of one half each
+//   warp 11     stores the outputs that warps 0-7 leave in shared memory, while
+//               they are at the next tile
+// A half of a group's accumulator has its own barriers and its own issuing warp:
+// the way from an MMA's end through the register sums to the next MMA into the
+// same columns (commit, sums, arrival at the even CTA: about 750 cycles) then has
+// to fit into the other three quarters of TMEM (768 cycles of MMA), not into one
+// half of it (512).  Persistent: a pair takes tiles a grid stride apart.
 // ---------------------------------------------------------------------------
-constexpr int kPairThreads = 320;
-constexpr int kPairStages = 6;
-constexpr uint32_t kPairStageBytes = 32768u;                 // 128 tokens + 128 columns of codes
-constexpr uint32_t kPairStagePitch = 33;                     // floats per staged output row (no bank conflicts)
+constexpr int kPairThreads = 384;
+constexpr int kPairStages = 5;
+constexpr uint32_t kPairStageBytes = 32768u;                 // 128 tokens, then 64 columns of either half
 constexpr uint32_t kPairStaging = kPairStages * kPairStageBytes;
-constexpr uint32_t kPairBytes = kPairStaging + 8u * 32u * kPairStagePitch * 4u;
+constexpr uint32_t kPairSlotBytes = 32768u;                  // 128 rows x 256 bytes of outputs, per half
+constexpr uint32_t kPairBytes = kPairStaging + 2u * kPairSlotBytes;
 constexpr uint32_t kPairDynBytes = kPairBytes + 1024u;
 constexpr int kPairRowGroup = 8;                             // token tiles that take their column tiles together
 
@@ -308,6 +299,52 @@ __device__ __forceinline__ void pair_tile(int t, int tiles_m, int tiles_n, int* 
     *tm = first + (r - *tn * rows);
 }
 
+// Whether any of the columns c0 .. c0 + 127 below N goes to an fp32 tensor: their
+// outputs then pass through shared memory as fp32 (64 columns at a time),
+// otherwise as bf16 (128 at a time).
+__device__ __forceinline__ bool block_is_wide(const OutRanges& out, int c0) {
+    bool wide = false;
+    for (int i = 0; i < out.n_outs; ++i)
+        wide |= out.f32[i] && out.begin[i] < c0 + 128 && out.begin[i + 1] > c0;
+    return wide;
+}
+
+// One slot of outputs (128 rows of 256 bytes, 16-byte chunk c of row r at c ^ (r & 15))
+// to global memory, by one warp: `cols` columns from c0, rows row0 .. below M.
+__device__ __forceinline__ void store_slot(const OutRanges& out, const uint8_t* slot, bool wide, int c0, int row0,
+                                           int M, int lane) {
+    const int cols = wide ? 64 : 128, elem = wide ? 4 : 2;
+    const int rows = M - row0 < 128 ? M - row0 : 128;
+    int r = 0;
+    while (r + 1 < out.n_outs && c0 >= out.begin[r + 1]) ++r;
+    const int64_t pitch = (int64_t)(out.begin[r + 1] - out.begin[r]) * elem;
+    const int64_t off = (int64_t)(c0 - out.begin[r]) * elem;
+    const bool dense = c0 + cols <= out.begin[r + 1] && (out.f32[r] != 0) == wide &&
+                       ((pitch | off | (int64_t)reinterpret_cast<uint64_t>(out.ptr[r])) & 15) == 0;
+    if (dense) {
+        // half a warp per row: whole 128-byte lines
+        uint8_t* p = (uint8_t*)out.ptr[r] + off + (lane & 15) * 16;
+        int j = lane >> 4;
+#pragma unroll 4
+        for (; j < rows; j += 2) {
+            const uint4 v = *reinterpret_cast<const uint4*>(slot + j * 256 + (((lane & 15) ^ (j & 15)) << 4));
+            *reinterpret_cast<uint4*>(p + (row0 + j) * pitch) = v;
+        }
+        return;
+    }
+    for (int q = lane; q < cols; q += 32) {                  // a lane per column
+        const OutColumn o(out, c0 + q);
+        if (!o.pitch) continue;
+        const int chunk = q * elem >> 4, in = q * elem & 15;
+        for (int j = 0; j < rows; ++j) {
+            const uint8_t* at = slot + j * 256 + ((chunk ^ (j & 15)) << 4) + in;
+            const float v = wide ? *reinterpret_cast<const float*>(at)
+                                 : __bfloat162float(*reinterpret_cast<const __nv_bfloat16*>(at));
+            o.store(row0 + j, v);
+        }
+    }
+}
+
 __global__ void __launch_bounds__(kPairThreads, 1)
 linear_pair_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUtensorMap map_x,
                    const float* __restrict__ sx, const float* __restrict__ sw, int M, int N, int groups,
@@ -315,7 +352,9 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_const
     constexpr int ST = kPairStages;
     extern __shared__ uint8_t dyn[];
     uint8_t* smem = align_smem<1024>(dyn);
-    __shared__ uint64_t full[ST], empty[ST], acc_full[2], acc_empty[2], drained;
+    __shared__ uint64_t full[ST], empty[ST];
+    __shared__ uint64_t acc_full[4], acc_empty[4];           // 2 * (group & 1) + half
+    __shared__ uint64_t slot_full[2], slot_free[2], drained[2];
     __shared__ uint32_t tmem_slot;
     __shared__ int gave_up;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -325,10 +364,11 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_const
 
     if (threadIdx.x == 0) {
         // full: the even CTA's, one arrival (its producer) and both CTAs' bytes;
-        // acc_empty: the even CTA's, eight warps of each CTA
-        for (int i = 0; i < ST; ++i) { mbar_init(&full[i], 1); mbar_init(&empty[i], 1); }
-        for (int i = 0; i < 2; ++i) { mbar_init(&acc_full[i], 1); mbar_init(&acc_empty[i], 16); }
-        mbar_init(&drained, 1);
+        // empty: a commit of either MMA warp; acc_empty: the even CTA's, four
+        // warps of each CTA
+        for (int i = 0; i < ST; ++i) { mbar_init(&full[i], 1); mbar_init(&empty[i], 2); }
+        for (int i = 0; i < 4; ++i) { mbar_init(&acc_full[i], 1); mbar_init(&acc_empty[i], 8); }
+        for (int i = 0; i < 2; ++i) { mbar_init(&slot_full[i], 4); mbar_init(&slot_free[i], 1); mbar_init(&drained[i], 1); }
         gave_up = 0;
         fence_mbar_init();
     }
@@ -348,7 +388,7 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_const
         for (int t = pair; t < tiles && ok; t += pairs) {
             int tm, tn;
             pair_tile(t, tiles_m, tiles_n, &tm, &tn);
-            const int m0 = tm * 256 + (int)rank * 128, n0 = tn * 256 + (int)rank * 128;
+            const int m0 = tm * 256 + (int)rank * 128, n0 = tn * 256 + (int)rank * 64;
             for (int g = 0; g < groups; ++g, ++i) {
                 if (i >= ST && !warp_wait(&empty[s], phase, &gave_up)) { ok = false; break; }
                 if (elect_one()) {
@@ -357,6 +397,7 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_const
                     uint8_t* st = smem + s * kPairStageBytes;
                     tma_load_2d_pair(st, &map_x, g * kFp8Group, m0, bar);
                     tma_load_2d_pair(st + 16384, &map_w, g * kFp8Group, n0, bar);
+                    tma_load_2d_pair(st + 24576, &map_w, g * kFp8Group, n0 + 128, bar);
                 }
                 __syncwarp();
                 if (++s == ST) { s = 0; phase ^= 1; }
@@ -365,52 +406,73 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_const
         // the last stages' releases must have landed before this CTA's shared
         // memory goes; after a give-up, so must its copies (they are counted
         // on the even CTA's barriers)
-        for (int j = i < ST ? 0 : i - ST; j < i; ++j)
-            if (!(*(volatile int*)&gave_up)) wait_or_give_up(&empty[j % ST], (j / ST) & 1, &gave_up);
-        if (*(volatile int*)&gave_up && rank == 0)
+        for (int j = i < ST ? 0 : i - ST; j < i && ok; ++j) ok = warp_wait(&empty[j % ST], (j / ST) & 1, &gave_up);
+        if (!ok && rank == 0)
             for (int j = i < ST ? 0 : i - ST; j < i; ++j) mbar_wait(&full[j % ST], (j / ST) & 1);
-    } else if (warp == 9) {
+    } else if (warp == 9 || warp == 10) {
         if (rank == 0) {
-            constexpr uint32_t idesc = idesc_e4m3_f32(256, 256);
+            constexpr uint32_t idesc = idesc_e4m3_f32(256, 128);
+            const int half = warp - 9;
             int i = 0, s = 0, phase = 0;
             bool ok = true;
             for (int t = pair; t < tiles && ok; t += pairs) {
                 for (int g = 0; g < groups; ++g, ++i) {
                     const int buf = i & 1;
-                    if ((i >= 2 && !warp_wait(&acc_empty[buf], ((i >> 1) & 1) ^ 1, &gave_up)) ||
-                        !warp_wait(&full[s], phase, &gave_up)) { ok = false; break; }
+                    if (!warp_wait(&full[s], phase, &gave_up) ||
+                        (i >= 2 && !warp_wait(&acc_empty[2 * buf + half], ((i >> 1) & 1) ^ 1, &gave_up))) { ok = false; break; }
                     tc_fence_after_sync();
                     if (elect_one()) {
                         const uint32_t a = smem_u32(smem + s * kPairStageBytes);
 #pragma unroll
-                        for (int j = 0; j < 4; ++j)
-                            mma_e4m3_pair(tmem + buf * 256, sw128_desc(a, 128, 0, 16 * j),
-                                          sw128_desc(a + 16384, 128, 0, 16 * j), idesc, j > 0);
+                        for (int j = 0; j < 4; ++j)      // 32 codes = 16 of the descriptor's 2-byte columns
+                            mma_e4m3_pair(tmem + buf * 256 + half * 128, sw128_desc(a, 128, 0, 16 * j),
+                                          sw128_desc(a + 16384 + half * 8192, 64, 0, 16 * j), idesc, j > 0);
+                        mma_commit_pair(&acc_full[2 * buf + half]);
                         mma_commit_pair(&empty[s]);
-                        mma_commit_pair(&acc_full[buf]);
                     }
                     __syncwarp();
                     if (++s == ST) { s = 0; phase ^= 1; }
                 }
             }
-            if (*(volatile int*)&gave_up) {
-                if (lane == 0) mma_commit_pair(&drained);
-                mbar_wait(&drained, 0);
+            if (!ok) {
+                if (lane == 0) mma_commit_pair(&drained[half]);
+                mbar_wait(&drained[half], 0);
             }
         }
-    } else {
-        const int half = warp >> 2;                          // columns half * 128 .. + 127 of the tile
-        const uint32_t lane0 = (uint32_t)((warp & 3) * 32) << 16;
-        float* stage = reinterpret_cast<float*>(smem + kPairStaging) + warp * 32 * kPairStagePitch;
-        const uint32_t bar0 = cluster_addr(smem_u32(&acc_empty[0]), 0);
-        const uint32_t bar1 = cluster_addr(smem_u32(&acc_empty[1]), 0);
-        int i = 0;
+    } else if (warp == 11) {
+        int jobs[2] = {0, 0};
         bool ok = true;
         for (int t = pair; t < tiles && ok; t += pairs) {
             int tm, tn;
             pair_tile(t, tiles_m, tiles_n, &tm, &tn);
-            const int row0 = tm * 256 + (int)rank * 128 + (warp & 3) * 32;
-            const int m = row0 + lane;
+            const int row0 = tm * 256 + (int)rank * 128;
+#pragma unroll
+            for (int half = 0; half < 2; ++half) {
+                const int c0 = tn * 256 + half * 128;
+                if (c0 >= N || !ok) break;
+                const bool wide = block_is_wide(out, c0);
+                for (int q = 0; q < (wide ? 2 : 1); ++q) {
+                    if (!warp_wait(&slot_full[half], jobs[half] & 1, &gave_up)) { ok = false; break; }
+                    store_slot(out, smem + kPairStaging + half * kPairSlotBytes, wide, c0 + q * 64, row0, M, lane);
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&slot_free[half]);
+                    ++jobs[half];
+                }
+            }
+        }
+    } else {
+        const int half = warp >> 2;                          // columns half * 128 .. + 127 of the tile
+        const int row = (warp & 3) * 32 + lane;              // row of the CTA's 128
+        const uint32_t at0 = tmem + ((uint32_t)((warp & 3) * 32) << 16) + half * 128;
+        uint8_t* slot = smem + kPairStaging + half * kPairSlotBytes + row * 256;
+        const uint32_t bar0 = cluster_addr(smem_u32(&acc_empty[half]), 0);
+        const uint32_t bar1 = cluster_addr(smem_u32(&acc_empty[2 + half]), 0);
+        int i = 0, jobs = 0;
+        bool ok = true;
+        for (int t = pair; t < tiles && ok; t += pairs) {
+            int tm, tn;
+            pair_tile(t, tiles_m, tiles_n, &tm, &tn);
+            const int m = tm * 256 + (int)rank * 128 + row;
             const int c0 = tn * 256 + half * 128;
             const float* sxp = sx + (int64_t)(m < M ? m : 0) * groups;
             const float* swp = sw + (int64_t)(c0 < N ? tn * 2 + half : 0) * groups;
@@ -420,12 +482,11 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_const
             float next = __ldg(sxp) * __ldg(swp);
             for (int g = 0; g < groups; ++g, ++i) {
                 const int buf = i & 1;
-                const float f = next;
+                const float2 f = make_float2(next, next);
                 if (g + 1 < groups) next = __ldg(sxp + g + 1) * __ldg(swp + g + 1);
-                if (!warp_wait(&acc_full[buf], (i >> 1) & 1, &gave_up)) { ok = false; break; }
+                if (!warp_wait(&acc_full[2 * buf + half], (i >> 1) & 1, &gave_up)) { ok = false; break; }
                 tc_fence_after_sync();
-                const uint32_t at = tmem + lane0 + buf * 256 + half * 128;
-                const float2 ff = make_float2(f, f);
+                const uint32_t at = at0 + buf * 256;
                 float d[2][16];
                 tmem_ld16(at, d[0]);
 #pragma unroll
@@ -434,54 +495,36 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_const
                     if (c < 7) tmem_ld16(at + 16 * (c + 1), d[(c + 1) & 1]);
 #pragma unroll
                     for (int q = 0; q < 8; ++q)
-                        acc[c * 8 + q] = __ffma2_rn(make_float2(d[c & 1][2 * q], d[c & 1][2 * q + 1]), ff, acc[c * 8 + q]);
+                        acc[c * 8 + q] = __ffma2_rn(make_float2(d[c & 1][2 * q], d[c & 1][2 * q + 1]), f, acc[c * 8 + q]);
                 }
                 tc_fence_before_sync();
                 __syncwarp();
                 if (lane == 0) mbar_arrive_cluster(buf ? bar1 : bar0);
             }
             if (!ok || c0 >= N) continue;
-            // Outputs: 128 columns inside one range, with rows that start on 32
-            // bytes, are stored by their threads (full 32-byte sectors); others go
-            // through shared memory, a lane per column.
-            int r = 0;
-            while (r + 1 < out.n_outs && c0 >= out.begin[r + 1]) ++r;
-            const int pitch = out.begin[r + 1] - out.begin[r], off = c0 - out.begin[r];
-            const int elem = out.f32[r] ? 4 : 2;
-            const bool direct = c0 + 128 <= out.begin[r + 1] && (pitch * elem) % 32 == 0 && (off * elem) % 32 == 0 &&
-                                (reinterpret_cast<uint64_t>(out.ptr[r]) & 31u) == 0;
-            if (direct) {
-                if (m < M) {
-                    uint8_t* p = (uint8_t*)out.ptr[r] + ((int64_t)m * pitch + off) * elem;
-                    if (elem == 4) {
+            if (block_is_wide(out, c0)) {
 #pragma unroll
-                        for (int c = 0; c < 64; c += 4) st_global_32(p + c * 8, __float_as_uint(acc[c].x), __float_as_uint(acc[c].y),
-                            __float_as_uint(acc[c + 1].x), __float_as_uint(acc[c + 1].y), __float_as_uint(acc[c + 2].x),
-                            __float_as_uint(acc[c + 2].y), __float_as_uint(acc[c + 3].x), __float_as_uint(acc[c + 3].y));
-                    } else {
+                for (int h = 0; h < 2; ++h) {
+                    if (jobs > 0 && !warp_wait(&slot_free[half], (jobs - 1) & 1, &gave_up)) { ok = false; break; }
 #pragma unroll
-                        for (int c = 0; c < 64; c += 8) st_global_32(p + c * 4, pack_bf16(acc[c].x, acc[c].y),
-                            pack_bf16(acc[c + 1].x, acc[c + 1].y), pack_bf16(acc[c + 2].x, acc[c + 2].y),
-                            pack_bf16(acc[c + 3].x, acc[c + 3].y), pack_bf16(acc[c + 4].x, acc[c + 4].y),
-                            pack_bf16(acc[c + 5].x, acc[c + 5].y), pack_bf16(acc[c + 6].x, acc[c + 6].y),
-                            pack_bf16(acc[c + 7].x, acc[c + 7].y));
-                    }
+                    for (int c = 0; c < 16; ++c)
+                        *reinterpret_cast<float4*>(slot + ((c ^ (row & 15)) << 4)) =
+                            make_float4(acc[h * 32 + 2 * c].x, acc[h * 32 + 2 * c].y, acc[h * 32 + 2 * c + 1].x,
+                                        acc[h * 32 + 2 * c + 1].y);
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&slot_full[half]);
+                    ++jobs;
                 }
-                continue;
-            }
-            const int rows = M - row0 < 32 ? M - row0 : 32;
+            } else {
+                if (jobs > 0 && !warp_wait(&slot_free[half], (jobs - 1) & 1, &gave_up)) { ok = false; continue; }
 #pragma unroll
-            for (int q = 0; q < 4; ++q) {
+                for (int c = 0; c < 16; ++c)
+                    *reinterpret_cast<uint4*>(slot + ((c ^ (row & 15)) << 4)) =
+                        make_uint4(pack_bf16(acc[4 * c].x, acc[4 * c].y), pack_bf16(acc[4 * c + 1].x, acc[4 * c + 1].y),
+                                   pack_bf16(acc[4 * c + 2].x, acc[4 * c + 2].y), pack_bf16(acc[4 * c + 3].x, acc[4 * c + 3].y));
                 __syncwarp();
-#pragma unroll
-                for (int c = 0; c < 16; ++c) {
-                    stage[lane * kPairStagePitch + 2 * c] = acc[q * 16 + c].x;
-                    stage[lane * kPairStagePitch + 2 * c + 1] = acc[q * 16 + c].y;
-                }
-                __syncwarp();
-                const OutColumn o(out, c0 + q * 32 + lane);
-                if (o.pitch)
-                    for (int j = 0; j < rows; ++j) o.store(row0 + j, stage[j * kPairStagePitch + lane]);
+                if (lane == 0) mbar_arrive(&slot_full[half]);
+                ++jobs;
             }
         }
     }
@@ -584,7 +627,7 @@ cudaError_t launch_pair(const gdr_linear_fp8_args& a, EncodeTiledFn enc, cudaStr
     if (tiles_m * tiles_n > (int64_t)INT32_MAX - 1024) return cudaErrorInvalidValue;
     CUtensorMap mw, mx;
     cudaError_t e;
-    if ((e = codes_map(enc, &mw, a.w, a.n, a.k, 128)) != cudaSuccess) return e;
+    if ((e = codes_map(enc, &mw, a.w, a.n, a.k, 64)) != cudaSuccess) return e;
     if ((e = codes_map(enc, &mx, a.x, a.rows, a.k, 128)) != cudaSuccess) return e;
     const int64_t pairs = tiles_m * tiles_n < 74 ? tiles_m * tiles_n : 74;
     return launch_cluster(linear_pair_kernel, dim3((unsigned)(2 * pairs)), dim3(kPairThreads), kPairDynBytes, 2, st,
