@@ -302,45 +302,57 @@ __device__ __forceinline__ void pair_tile(int t, int tiles_m, int tiles_n, int* 
 // Whether any of the columns c0 .. c0 + 127 below N goes to an fp32 tensor: their
 // outputs then pass through shared memory as fp32 (64 columns at a time),
 // otherwise as bf16 (128 at a time).
-__device__ __forceinline__ bool block_is_wide(const OutRanges& out, int c0) {
+__device__ __forceinline__ bool block_is_wide(const OutRanges& out, int c0, int lane) {
     bool wide = false;
-    for (int i = 0; i < out.n_outs; ++i)
-        wide |= out.f32[i] && out.begin[i] < c0 + 128 && out.begin[i + 1] > c0;
-    return wide;
+    if (lane < out.n_outs) wide = out.f32[lane] && out.begin[lane] < c0 + 128 && out.begin[lane + 1] > c0;
+    return __any_sync(0xffffffffu, wide);
 }
 
-// One slot of outputs (128 rows of 256 bytes, 16-byte chunk c of row r at c ^ (r & 15))
-// to global memory, by one warp: `cols` columns from c0, rows row0 .. below M.
-__device__ __forceinline__ void store_slot(const OutRanges& out, const uint8_t* slot, bool wide, int c0, int row0,
-                                           int M, int lane) {
+// Where the 16-byte chunk c (0 .. 15) of a row's 256 bytes lies in an output slot:
+// two boxes of 128 rows x 128 bytes, 128-byte swizzle (no bank conflicts, and the
+// layout a TMA store reads).
+__device__ __forceinline__ uint32_t slot_chunk(int row, int c) {
+    return (uint32_t)((c >> 3) * 16384 + row * 128 + (((c & 7) ^ (row & 7)) << 4));
+}
+
+// The tensors of the output ranges; a range whose base or rows are not 16-byte
+// aligned has none.
+struct OutMaps {
+    CUtensorMap map[GDR_LINEAR_MAX_OUTS];
+    int valid[GDR_LINEAR_MAX_OUTS];
+};
+
+// One slot of outputs to global memory, by one warp: columns from c0 (128 of bf16,
+// 64 of fp32), rows row0 .. below M.  A block of columns inside one range goes by
+// two TMA stores (which drop what lies past the tensor's rows and columns), others
+// element by element, a lane per column.
+__device__ __forceinline__ void store_slot(const OutRanges& out, const OutMaps& maps, const uint8_t* slot, bool wide,
+                                           int c0, int row0, int M, int lane) {
     const int cols = wide ? 64 : 128, elem = wide ? 4 : 2;
-    const int rows = M - row0 < 128 ? M - row0 : 128;
     int r = 0;
     while (r + 1 < out.n_outs && c0 >= out.begin[r + 1]) ++r;
-    const int64_t pitch = (int64_t)(out.begin[r + 1] - out.begin[r]) * elem;
-    const int64_t off = (int64_t)(c0 - out.begin[r]) * elem;
-    const bool dense = c0 + cols <= out.begin[r + 1] && (out.f32[r] != 0) == wide &&
-                       ((pitch | off | (int64_t)reinterpret_cast<uint64_t>(out.ptr[r])) & 15) == 0;
-    if (dense) {
-        // half a warp per row: whole 128-byte lines
-        uint8_t* p = (uint8_t*)out.ptr[r] + off + (lane & 15) * 16;
-        int j = lane >> 4;
-#pragma unroll 4
-        for (; j < rows; j += 2) {
-            const uint4 v = *reinterpret_cast<const uint4*>(slot + j * 256 + (((lane & 15) ^ (j & 15)) << 4));
-            *reinterpret_cast<uint4*>(p + (row0 + j) * pitch) = v;
+    const int off = c0 - out.begin[r];
+    if ((c0 + cols <= out.begin[r + 1] || r + 1 == out.n_outs) && (out.f32[r] != 0) == wide && maps.valid[r] &&
+        (off * elem & 15) == 0) {
+        if (row0 < M && elect_one()) {
+            tma_store_2d(&maps.map[r], slot, off, row0);
+            if (c0 + cols / 2 < out.begin[r + 1]) tma_store_2d(&maps.map[r], slot + 16384, off + cols / 2, row0);
+            bulk_commit_group();
+            bulk_wait_group_read0();
         }
+        __syncwarp();
         return;
     }
-    for (int q = lane; q < cols; q += 32) {                  // a lane per column
+    const int rows = M - row0 < 128 ? M - row0 : 128;
+    for (int q = lane; q < cols; q += 32) {
         const OutColumn o(out, c0 + q);
         if (!o.pitch) continue;
         const int chunk = q * elem >> 4, in = q * elem & 15;
+#pragma unroll 8
         for (int j = 0; j < rows; ++j) {
-            const uint8_t* at = slot + j * 256 + ((chunk ^ (j & 15)) << 4) + in;
-            const float v = wide ? *reinterpret_cast<const float*>(at)
-                                 : __bfloat162float(*reinterpret_cast<const __nv_bfloat16*>(at));
-            o.store(row0 + j, v);
+            const uint8_t* at = slot + slot_chunk(j, chunk) + in;
+            o.store(row0 + j, wide ? *reinterpret_cast<const float*>(at)
+                                   : __bfloat162float(*reinterpret_cast<const __nv_bfloat16*>(at)));
         }
     }
 }
@@ -348,7 +360,8 @@ __device__ __forceinline__ void store_slot(const OutRanges& out, const uint8_t* 
 __global__ void __launch_bounds__(kPairThreads, 1)
 linear_pair_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUtensorMap map_x,
                    const float* __restrict__ sx, const float* __restrict__ sw, int M, int N, int groups,
-                   int tiles_m, int tiles_n, const __grid_constant__ OutRanges out) {
+                   int tiles_m, int tiles_n, const __grid_constant__ OutRanges out,
+                   const __grid_constant__ OutMaps maps) {
     constexpr int ST = kPairStages;
     extern __shared__ uint8_t dyn[];
     uint8_t* smem = align_smem<1024>(dyn);
@@ -382,6 +395,8 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_const
     pdl_wait();
     pdl_launch_dependents();
 
+    // registers: 256 threads x 216 + 128 x 72 = the launch's 384 x 168
+    if (warp >= 8) asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
     if (warp == 8) {
         int i = 0, s = 0, phase = 1;
         bool ok = true;
@@ -450,40 +465,70 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_const
             for (int half = 0; half < 2; ++half) {
                 const int c0 = tn * 256 + half * 128;
                 if (c0 >= N || !ok) break;
-                const bool wide = block_is_wide(out, c0);
+                const bool wide = block_is_wide(out, c0, lane);
                 for (int q = 0; q < (wide ? 2 : 1); ++q) {
                     if (!warp_wait(&slot_full[half], jobs[half] & 1, &gave_up)) { ok = false; break; }
-                    store_slot(out, smem + kPairStaging + half * kPairSlotBytes, wide, c0 + q * 64, row0, M, lane);
+                    store_slot(out, maps, smem + kPairStaging + half * kPairSlotBytes, wide, c0 + q * 64, row0, M, lane);
                     __syncwarp();
                     if (lane == 0) mbar_arrive(&slot_free[half]);
                     ++jobs[half];
                 }
             }
         }
+        if (elect_one()) bulk_wait_group0();
     } else {
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
         const int half = warp >> 2;                          // columns half * 128 .. + 127 of the tile
         const int row = (warp & 3) * 32 + lane;              // row of the CTA's 128
         const uint32_t at0 = tmem + ((uint32_t)((warp & 3) * 32) << 16) + half * 128;
-        uint8_t* slot = smem + kPairStaging + half * kPairSlotBytes + row * 256;
+        uint8_t* slot = smem + kPairStaging + half * kPairSlotBytes;
         const uint32_t bar0 = cluster_addr(smem_u32(&acc_empty[half]), 0);
         const uint32_t bar1 = cluster_addr(smem_u32(&acc_empty[2 + half]), 0);
+        const bool vec = (groups & 3) == 0 &&
+                         ((reinterpret_cast<uint64_t>(sx) | reinterpret_cast<uint64_t>(sw)) & 15) == 0;
         int i = 0, jobs = 0;
         bool ok = true;
-        for (int t = pair; t < tiles && ok; t += pairs) {
+        // this tile's factor rows; the first four groups' factors are fetched a tile ahead
+        const float *sxp = sx, *swp = sw;
+        int c0 = 0;
+        float4 nx, nw;
+        const auto fetch = [&](int g) {
+            if (vec) {
+                nx = __ldg(reinterpret_cast<const float4*>(sxp + g));
+                nw = __ldg(reinterpret_cast<const float4*>(swp + g));
+            } else {
+                const int last = groups - 1;
+                nx = make_float4(__ldg(sxp + g), __ldg(sxp + min(g + 1, last)), __ldg(sxp + min(g + 2, last)),
+                                 __ldg(sxp + min(g + 3, last)));
+                nw = make_float4(__ldg(swp + g), __ldg(swp + min(g + 1, last)), __ldg(swp + min(g + 2, last)),
+                                 __ldg(swp + min(g + 3, last)));
+            }
+        };
+        const auto enter = [&](int t) {
             int tm, tn;
             pair_tile(t, tiles_m, tiles_n, &tm, &tn);
             const int m = tm * 256 + (int)rank * 128 + row;
-            const int c0 = tn * 256 + half * 128;
-            const float* sxp = sx + (int64_t)(m < M ? m : 0) * groups;
-            const float* swp = sw + (int64_t)(c0 < N ? tn * 2 + half : 0) * groups;
+            c0 = tn * 256 + half * 128;
+            sxp = sx + (int64_t)(m < M ? m : 0) * groups;
+            swp = sw + (int64_t)(c0 < N ? tn * 2 + half : 0) * groups;
+            fetch(0);
+        };
+        if (pair < tiles) enter(pair);
+        for (int t = pair; t < tiles && ok; t += pairs) {
             float2 acc[64];
 #pragma unroll
             for (int c = 0; c < 64; ++c) acc[c] = make_float2(0.f, 0.f);
-            float next = __ldg(sxp) * __ldg(swp);
+            float4 fs = make_float4(0.f, 0.f, 0.f, 0.f);
             for (int g = 0; g < groups; ++g, ++i) {
                 const int buf = i & 1;
-                const float2 f = make_float2(next, next);
-                if (g + 1 < groups) next = __ldg(sxp + g + 1) * __ldg(swp + g + 1);
+                if ((g & 3) == 0) {
+                    fs = make_float4(nx.x * nw.x, nx.y * nw.y, nx.z * nw.z, nx.w * nw.w);
+                    if (g + 4 < groups) fetch(g + 4);
+                }
+                const float2 f = make_float2(fs.x, fs.x);
+                fs.x = fs.y;
+                fs.y = fs.z;
+                fs.z = fs.w;
                 if (!warp_wait(&acc_full[2 * buf + half], (i >> 1) & 1, &gave_up)) { ok = false; break; }
                 tc_fence_after_sync();
                 const uint32_t at = at0 + buf * 256;
@@ -501,16 +546,19 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_const
                 __syncwarp();
                 if (lane == 0) mbar_arrive_cluster(buf ? bar1 : bar0);
             }
-            if (!ok || c0 >= N) continue;
-            if (block_is_wide(out, c0)) {
+            const int c_out = c0;
+            if (t + pairs < tiles) enter(t + pairs);
+            if (!ok || c_out >= N) continue;
+            if (block_is_wide(out, c_out, lane)) {
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
                     if (jobs > 0 && !warp_wait(&slot_free[half], (jobs - 1) & 1, &gave_up)) { ok = false; break; }
 #pragma unroll
                     for (int c = 0; c < 16; ++c)
-                        *reinterpret_cast<float4*>(slot + ((c ^ (row & 15)) << 4)) =
+                        *reinterpret_cast<float4*>(slot + slot_chunk(row, c)) =
                             make_float4(acc[h * 32 + 2 * c].x, acc[h * 32 + 2 * c].y, acc[h * 32 + 2 * c + 1].x,
                                         acc[h * 32 + 2 * c + 1].y);
+                    fence_proxy_async_smem();
                     __syncwarp();
                     if (lane == 0) mbar_arrive(&slot_full[half]);
                     ++jobs;
@@ -519,9 +567,10 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_const
                 if (jobs > 0 && !warp_wait(&slot_free[half], (jobs - 1) & 1, &gave_up)) { ok = false; continue; }
 #pragma unroll
                 for (int c = 0; c < 16; ++c)
-                    *reinterpret_cast<uint4*>(slot + ((c ^ (row & 15)) << 4)) =
+                    *reinterpret_cast<uint4*>(slot + slot_chunk(row, c)) =
                         make_uint4(pack_bf16(acc[4 * c].x, acc[4 * c].y), pack_bf16(acc[4 * c + 1].x, acc[4 * c + 1].y),
                                    pack_bf16(acc[4 * c + 2].x, acc[4 * c + 2].y), pack_bf16(acc[4 * c + 3].x, acc[4 * c + 3].y));
+                fence_proxy_async_smem();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&slot_full[half]);
                 ++jobs;
@@ -565,6 +614,18 @@ cudaError_t codes_map(EncodeTiledFn enc, CUtensorMap* m, const void* base, int64
     const CUresult r = enc(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(base), dims, strides, box,
                            estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
                            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
+}
+
+// Map of an output tensor [rows][cols], box 128 rows x 128 bytes, 128-byte swizzle.
+cudaError_t out_map(EncodeTiledFn enc, CUtensorMap* m, void* base, int64_t rows, int cols, int elem) {
+    const cuuint64_t dims[2] = {(cuuint64_t)cols, (cuuint64_t)rows};
+    const cuuint64_t strides[1] = {(cuuint64_t)cols * elem};
+    const cuuint32_t box[2] = {(cuuint32_t)(128 / elem), 128u};
+    const cuuint32_t estr[2] = {1u, 1u};
+    const CUresult r = enc(m, elem == 4 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, base,
+                           dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                           CU_TENSOR_MAP_L2_PROMOTION_NONE, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
     return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
 }
 
@@ -629,10 +690,18 @@ cudaError_t launch_pair(const gdr_linear_fp8_args& a, EncodeTiledFn enc, cudaStr
     cudaError_t e;
     if ((e = codes_map(enc, &mw, a.w, a.n, a.k, 64)) != cudaSuccess) return e;
     if ((e = codes_map(enc, &mx, a.x, a.rows, a.k, 128)) != cudaSuccess) return e;
+    OutMaps maps;
+    memset(&maps, 0, sizeof(maps));
+    for (int i = 0; i < a.n_outs; ++i) {
+        const int elem = a.out_dtype[i] == GDR_F32 ? 4 : 2;
+        if ((int64_t)a.out_cols[i] * elem % 16 != 0 || (reinterpret_cast<uintptr_t>(a.out[i]) & 15u) != 0) continue;
+        if ((e = out_map(enc, &maps.map[i], a.out[i], a.rows, a.out_cols[i], elem)) != cudaSuccess) return e;
+        maps.valid[i] = 1;
+    }
     const int64_t pairs = tiles_m * tiles_n < 74 ? tiles_m * tiles_n : 74;
     return launch_cluster(linear_pair_kernel, dim3((unsigned)(2 * pairs)), dim3(kPairThreads), kPairDynBytes, 2, st,
                           mw, mx, a.x_scale, a.w_scale, (int)a.rows, a.n, groups, (int)tiles_m, (int)tiles_n,
-                          out_ranges(a));
+                          out_ranges(a), maps);
 }
 
 }  // namespace

@@ -116,6 +116,13 @@ __device__ __forceinline__ void tma_load_2d(void* smem_dst, const void* tensor_m
           "r"(smem_u32(bar)) : "memory");
 }
 
+// One tiled 2-D TMA store of a box from shared memory; what lies past the
+// tensor's ends is not written.  Tracked by bulk groups.
+__device__ __forceinline__ void tma_store_2d(const void* tensor_map, const void* smem_src, int x, int y) {
+    asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.tile.bulk_group [%0, {%1, %2}], [%3];"
+                 ::"l"(reinterpret_cast<uint64_t>(tensor_map)), "r"(x), "r"(y), "r"(smem_u32(smem_src)) : "memory");
+}
+
 // L2 cache policies for the copies below: keep (data read again soon, e.g. a
 // chunk record the sequential pass reads next) or drop first (read once).
 __device__ __forceinline__ uint64_t l2_policy_evict_last() {
