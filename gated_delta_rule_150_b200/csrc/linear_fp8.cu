@@ -59,10 +59,11 @@ struct OutColumn {
 // slower.
 constexpr int kWaitTries = 1 << 20;
 
+template <bool CLUSTER = false>          // whether the phase orders other CTAs' writes
 __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, int* gave_up) {
     const uint32_t a = smem_u32(bar);
     for (int i = 0; i < kWaitTries; ++i)
-        if (__all_sync(0xffffffffu, mbar_try_wait(a, parity))) return true;
+        if (__all_sync(0xffffffffu, CLUSTER ? mbar_try_wait_cluster(a, parity) : mbar_try_wait(a, parity))) return true;
     *gave_up = 1;
     atomicOr(&g_linear_error, 1u);
     return false;
@@ -72,35 +73,41 @@ __device__ __forceinline__ void mbar_arrive(uint64_t* bar) {
     asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_u32(bar)) : "memory");
 }
 
-// Read a float of CTA `rank` of the cluster at the place `addr` of this CTA.
-__device__ __forceinline__ float ld_cluster(uint32_t addr, uint32_t rank) {
-    float v;
-    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(cluster_addr(addr, rank)) : "memory");
-    return v;
+// 16 bytes to another CTA's shared memory (shared::cluster addresses), counted on
+// a barrier there.
+__device__ __forceinline__ void st_async4(uint32_t cluster_dst, const float4& v, uint32_t cluster_bar) {
+    asm volatile("st.async.weak.shared::cluster.mbarrier::complete_tx::bytes.v4.b32 [%0], {%1, %2, %3, %4}, [%5];"
+                 ::"r"(cluster_dst), "r"(__float_as_uint(v.x)), "r"(__float_as_uint(v.y)), "r"(__float_as_uint(v.z)),
+                   "r"(__float_as_uint(v.w)), "r"(cluster_bar) : "memory");
 }
 
 // ---------------------------------------------------------------------------
 // Few tokens: the weights take the MMA's 128-row side and BN tokens its other
 // side, so a decode step's few tokens do not leave the tensor core's rows empty
 // and every weight is fetched once per BN tokens.  A cluster of `split` CTAs
-// shares one 128-column tile: each sums a range of the K groups, and the parts
-// meet through distributed shared memory in rank order (no atomics, no
-// workspace).
+// shares one 128-column tile: each sums a range of the K groups and sends its
+// part of every four tokens to the CTA that owns them (4-token group q: CTA
+// q % split), which adds the parts in rank order and stores.  The parts arrive in
+// a place of their own and are counted on a barrier, so nobody waits for the
+// whole cluster at the end: no atomics, no workspace.
 //   warps 0-3   a thread owns an output column, BN fp32 sums (one per token)
-//   warp 4      TMA loads (one lane)
-//   warp 5      TMEM allocation, MMAs (one lane)
+//   warp 4      TMA loads
+//   warp 5      TMEM allocation, MMAs
 // ---------------------------------------------------------------------------
 constexpr int kFewThreads = 192;
+constexpr int kFewRows = 64;
 
 template <int BN>
 struct FewLayout {
     static constexpr uint32_t kStageBytes = 16384u + BN * 128u;
-    static constexpr int kStages = BN <= 32 ? 6 : BN <= 64 ? 5 : 4;
-    static constexpr uint32_t kFactors = kStages * kStageBytes;         // 4 warps x 2 x BN floats
-    static constexpr uint32_t kBytes = kFactors + 4u * 2u * BN * 4u;
+    static constexpr int kStages = BN <= 16 ? 5 : BN <= 32 ? 4 : 3;     // two CTAs per SM
+    static constexpr int kGroups = BN / 4;                              // of four tokens
+    static constexpr uint32_t kParts = kStages * kStageBytes;           // [slot][rank][column] x 4 tokens
+    static constexpr uint32_t kPartBytes = 2048u;
+    static constexpr uint32_t kFactors = kParts + (kGroups < 8 ? 8 : kGroups) * kPartBytes;
+    static constexpr uint32_t kBytes = kFactors + 4u * 2u * BN * 4u;    // 4 warps x 2 x BN floats
     static constexpr uint32_t kDynBytes = kBytes + 1024u;               // 1024-byte alignment
     static constexpr uint32_t kTmemCols = 2 * BN < 32 ? 32 : 2 * BN;
-    static_assert((uint32_t)BN * 512u <= kFactors, "the parts take the stages' place");
 };
 
 template <int BN>
@@ -112,22 +119,32 @@ linear_few_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_consta
     constexpr int ST = Lay::kStages;
     extern __shared__ uint8_t dyn[];
     uint8_t* smem = align_smem<1024>(dyn);
-    __shared__ uint64_t full[ST], empty[ST], acc_full[2], acc_empty[2], drained;
+    __shared__ uint64_t full[ST], empty[ST], acc_full[2], acc_empty[2], drained, parts_bar;
     __shared__ uint32_t tmem_slot;
     __shared__ int gave_up;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int tile = blockIdx.x / split, part = blockIdx.x - tile * split;
     const int n0 = tile * 128, m0 = blockIdx.y * BN;
+    const int tokens = M - m0 < BN ? M - m0 : BN;
     const int g0 = (int)((int64_t)groups * part / split), g1 = (int)((int64_t)groups * (part + 1) / split);
     const int count = g1 - g0;
+    const int quads = (tokens + 3) >> 2;
+    const int owned = quads > part ? (quads - part + split - 1) / split : 0;     // quads part, part + split, ...
 
     if (threadIdx.x == 0) {
         for (int i = 0; i < ST; ++i) { mbar_init(&full[i], 1); mbar_init(&empty[i], 1); }
         for (int i = 0; i < 2; ++i) { mbar_init(&acc_full[i], 1); mbar_init(&acc_empty[i], 4); }
         mbar_init(&drained, 1);
+        mbar_init(&parts_bar, 1);
         gave_up = 0;
         fence_mbar_init();
+        if (split > 1) mbar_arrive_expect_tx(&parts_bar, (uint32_t)(owned * split) * Lay::kPartBytes);
     }
+    // Every CTA's barrier must be ready for its peers' parts.  TMEM is held only
+    // where no other CTA is waited for (before this and after the sums), so that
+    // clusters which share SMs cannot wait for each other's columns.
+    __syncwarp();
+    if (split > 1) cluster_sync();
     if (warp == 5) tmem_alloc(&tmem_slot, Lay::kTmemCols);
     tc_fence_before_sync();
     __syncthreads();
@@ -136,11 +153,11 @@ linear_few_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_consta
     pdl_wait();
     pdl_launch_dependents();
 
-    float acc[BN];
     if (warp == 4) {
         int i = 0;
+        bool ok = true;
         for (int s = 0, phase = 1; i < count; ++i) {
-            if (i >= ST && !warp_wait(&empty[s], phase, &gave_up)) break;
+            if (i >= ST && !warp_wait(&empty[s], phase, &gave_up)) { ok = false; break; }
             if (elect_one()) {
                 uint8_t* st = smem + s * Lay::kStageBytes;
                 mbar_arrive_expect_tx(&full[s], Lay::kStageBytes);
@@ -151,14 +168,15 @@ linear_few_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_consta
             if (++s == ST) { s = 0; phase ^= 1; }
         }
         // gave up: no copy may still be in flight when the CTA ends
-        if (*(volatile int*)&gave_up)
+        if (!ok)
             for (int j = i < ST ? 0 : i - ST; j < i; ++j) mbar_wait(&full[j % ST], (j / ST) & 1);
     } else if (warp == 5) {
         constexpr uint32_t idesc = idesc_e4m3_f32(128, BN);
+        bool ok = true;
         for (int i = 0, s = 0, phase = 0; i < count; ++i) {
             const int buf = i & 1;
-            if (i >= 2 && !warp_wait(&acc_empty[buf], ((i >> 1) & 1) ^ 1, &gave_up)) break;
-            if (!warp_wait(&full[s], phase, &gave_up)) break;
+            if (!warp_wait(&full[s], phase, &gave_up) ||
+                (i >= 2 && !warp_wait(&acc_empty[buf], ((i >> 1) & 1) ^ 1, &gave_up))) { ok = false; break; }
             tc_fence_after_sync();
             if (elect_one()) {
                 const uint32_t a = smem_u32(smem + s * Lay::kStageBytes);
@@ -172,26 +190,32 @@ linear_few_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_consta
             __syncwarp();
             if (++s == ST) { s = 0; phase ^= 1; }
         }
-        if (*(volatile int*)&gave_up) {
+        if (!ok) {
             if (lane == 0) mma_commit(&drained);
             mbar_wait(&drained, 0);
         }
+        __syncwarp();
+        asm volatile("bar.sync 1, 160;" ::: "memory");       // warps 0-3 have read their sums
+        tc_fence_after_sync();
+        tmem_dealloc(tmem, Lay::kTmemCols);
     } else {
+        float acc[BN];
 #pragma unroll
         for (int m = 0; m < BN; ++m) acc[m] = 0.f;
         float* factors = reinterpret_cast<float*>(smem + Lay::kFactors) + warp * 2 * BN;
-        constexpr int kPer = (BN + 31) / 32;
+        constexpr int kPer = (BN + 31) / 32, kLoad = BN < 32 ? BN : 32;
         float next[kPer];
         const float* swp = sw + (int64_t)tile * groups;
         const auto fetch = [&](int g) {
             const float w = __ldg(swp + g);
 #pragma unroll
             for (int p = 0; p < kPer; ++p) {
-                const int m = m0 + p * 32 + lane;
-                next[p] = (BN >= 32 || lane < BN) && m < M ? __ldg(sx + (int64_t)m * groups + g) * w : 0.f;
+                const int m = p * 32 + lane;
+                next[p] = m < tokens ? __ldg(sx + (int64_t)(m0 + m) * groups + g) * w : 0.f;
             }
         };
-        if (count > 0) fetch(g0);
+        fetch(g0);
+        bool ok = true;
         for (int i = 0; i < count; ++i) {
             const int buf = i & 1;
             float* f = factors + buf * BN;
@@ -200,65 +224,75 @@ linear_few_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_consta
                 if (BN >= 32 || lane < BN) f[p * 32 + lane] = next[p];
             if (i + 1 < count) fetch(g0 + i + 1);
             __syncwarp();
-            if (!warp_wait(&acc_full[buf], (i >> 1) & 1, &gave_up)) break;
+            if (!warp_wait(&acc_full[buf], (i >> 1) & 1, &gave_up)) { ok = false; break; }
             tc_fence_after_sync();
+            const uint32_t at = tmem + ((uint32_t)(warp * 32) << 16) + buf * BN;
+            float d[BN / kLoad][kLoad];
 #pragma unroll
-            for (int c = 0; c < BN; c += 16) {
-                float d[16];
-                tmem_ld16(tmem + ((uint32_t)(warp * 32) << 16) + buf * BN + c, d);
-                tmem_ld_wait_for(d);
+            for (int c = 0; c < BN / kLoad; ++c) tmem_ld(at + c * kLoad, d[c]);
 #pragma unroll
-                for (int q = 0; q < 16; q += 4) {
-                    const float4 w = *reinterpret_cast<const float4*>(f + c + q);
-                    acc[c + q] = fmaf(d[q], w.x, acc[c + q]);
-                    acc[c + q + 1] = fmaf(d[q + 1], w.y, acc[c + q + 1]);
-                    acc[c + q + 2] = fmaf(d[q + 2], w.z, acc[c + q + 2]);
-                    acc[c + q + 3] = fmaf(d[q + 3], w.w, acc[c + q + 3]);
+            for (int c = 0; c < BN / kLoad; ++c) {
+                tmem_ld_wait_for(d[c]);
+#pragma unroll
+                for (int q = 0; q < kLoad; q += 4) {
+                    const float4 w = *reinterpret_cast<const float4*>(f + c * kLoad + q);
+                    float* o = acc + c * kLoad + q;
+                    o[0] = fmaf(d[c][q], w.x, o[0]);
+                    o[1] = fmaf(d[c][q + 1], w.y, o[1]);
+                    o[2] = fmaf(d[c][q + 2], w.z, o[2]);
+                    o[3] = fmaf(d[c][q + 3], w.w, o[3]);
                 }
             }
             tc_fence_before_sync();
             __syncwarp();
             if (lane == 0) mbar_arrive(&acc_empty[buf]);
         }
-    }
-
-    const int tokens = M - m0 < BN ? M - m0 : BN;
-    if (split == 1) {
-        if (warp < 4) {
-            const OutColumn o(out, n0 + threadIdx.x);
+        tc_fence_before_sync();
+        asm volatile("bar.arrive 1, 160;" ::: "memory");
+        const OutColumn o(out, n0 + threadIdx.x);
+        if (split == 1) {
             if (o.pitch)
 #pragma unroll
                 for (int m = 0; m < BN; ++m)
                     if (m < tokens) o.store(m0 + m, acc[m]);
-        }
-        __syncthreads();
-        if (warp == 5) tmem_dealloc(tmem, Lay::kTmemCols);
-        return;
-    }
-    // This CTA's part, [token][column], where the stages were: every MMA that
-    // read them has completed.
-    __syncthreads();
-    float* parts = reinterpret_cast<float*>(smem);
-    if (warp < 4) {
+        } else {
+            const uint32_t to = smem_u32(smem + Lay::kParts) + part * Lay::kPartBytes + threadIdx.x * 16;
+            const uint32_t bar = smem_u32(&parts_bar);
+            int owner = 0, slot = 0;                 // of quad q: q % split, q / split
 #pragma unroll
-        for (int m = 0; m < BN; ++m)
-            if (m < tokens) parts[m * 128 + threadIdx.x] = acc[m];
-    }
-    // TMEM is given back before the CTA waits for its peers
-    if (warp == 5) tmem_dealloc(tmem, Lay::kTmemCols);
-    __syncwarp();
-    cluster_sync();
-    if (warp < 4) {
-        const OutColumn o(out, n0 + threadIdx.x);
-        for (int m = part; m < tokens; m += split) {
-            const uint32_t at = smem_u32(parts + m * 128 + threadIdx.x);
-            float v = 0.f;
-            for (int r = 0; r < split; ++r) v += ld_cluster(at, r);
-            if (o.pitch) o.store(m0 + m, v);
+            for (int q = 0; q < Lay::kGroups; ++q) {
+                if (q < quads)
+                    st_async4(cluster_addr(to + slot * split * Lay::kPartBytes, owner),
+                              make_float4(acc[4 * q], acc[4 * q + 1], acc[4 * q + 2], acc[4 * q + 3]),
+                              cluster_addr(bar, owner));
+                if (++owner == split) { owner = 0; ++slot; }
+            }
+            if (owned > 0 && warp_wait<true>(&parts_bar, 0, &gave_up)) {
+                const float4* parts = reinterpret_cast<const float4*>(smem + Lay::kParts) + threadIdx.x;
+                for (int j = 0; j < owned; ++j) {
+                    float4 v = parts[(j * split) * 128];
+                    for (int r = 1; r < split; ++r) {
+                        const float4 p = parts[(j * split + r) * 128];
+                        v.x += p.x; v.y += p.y; v.z += p.z; v.w += p.w;
+                    }
+                    const int m = (part + j * split) * 4;
+                    if (o.pitch) {
+                        o.store(m0 + m, v.x);
+                        if (m + 1 < tokens) o.store(m0 + m + 1, v.y);
+                        if (m + 2 < tokens) o.store(m0 + m + 2, v.z);
+                        if (m + 3 < tokens) o.store(m0 + m + 3, v.w);
+                    }
+                }
+            }
         }
     }
-    __syncwarp();
-    cluster_sync();
+    if (split > 1) {
+        // no CTA may end while a part is on its way to it; owners have waited for
+        // theirs, so nothing else has to be ordered here
+        __syncwarp();
+        asm volatile("barrier.cluster.arrive.relaxed.aligned;\n\tbarrier.cluster.wait.aligned;" ::: "memory");
+        if (*(volatile int*)&gave_up) __nanosleep(100000);
+    }
 }
 
 // ---------------------------------------------------------------------------
@@ -668,18 +702,17 @@ cudaError_t launch_few(const gdr_linear_fp8_args& a, EncodeTiledFn enc, cudaStre
     const int groups = fp8_groups(a.k), tiles = fp8_groups(a.n);
     const int64_t token_tiles = (a.rows + BN - 1) / BN;
     if (token_tiles > 65535) return cudaErrorInvalidValue;
-    // as many parts of K as fill the SMs twice, none without work
-    int64_t split = 2 * 148 / (tiles * token_tiles);
-    split = split < 1 ? 1 : split > 8 ? 8 : split;
-    if (split > groups) split = groups;
-    if (tiles * split > (int64_t)INT32_MAX) return cudaErrorInvalidValue;
+    // as many parts of K (a power of two) as fill the SMs twice, none without work
+    int split = 1;
+    while (split < 8 && 2 * split <= groups && 2 * split * tiles * token_tiles <= 2 * 148) split *= 2;
+    if ((int64_t)tiles * split > (int64_t)INT32_MAX) return cudaErrorInvalidValue;
     CUtensorMap mw, mx;
     cudaError_t e;
     if ((e = codes_map(enc, &mw, a.w, a.n, a.k, 128)) != cudaSuccess) return e;
     if ((e = codes_map(enc, &mx, a.x, a.rows, a.k, BN)) != cudaSuccess) return e;
     return launch_cluster(linear_few_kernel<BN>, dim3((unsigned)(tiles * split), (unsigned)token_tiles),
-                          dim3(kFewThreads), FewLayout<BN>::kDynBytes, (int)split, st, mw, mx, a.x_scale,
-                          a.w_scale, (int)a.rows, groups, (int)split, out_ranges(a));
+                          dim3(kFewThreads), FewLayout<BN>::kDynBytes, split, st, mw, mx, a.x_scale,
+                          a.w_scale, (int)a.rows, groups, split, out_ranges(a));
 }
 
 cudaError_t launch_pair(const gdr_linear_fp8_args& a, EncodeTiledFn enc, cudaStream_t st) {
@@ -712,8 +745,7 @@ cudaError_t launch_linear_fp8(const gdr_linear_fp8_args& a, cudaStream_t st) {
     if (e != cudaSuccess) return e;
     if (a.rows <= 16) return launch_few<16>(a, enc, st);
     if (a.rows <= 32) return launch_few<32>(a, enc, st);
-    if (a.rows <= 64) return launch_few<64>(a, enc, st);
-    if (a.rows <= 512) return launch_few<128>(a, enc, st);
+    if (a.rows <= kFewRows) return launch_few<64>(a, enc, st);
     return launch_pair(a, enc, st);
 }
 
