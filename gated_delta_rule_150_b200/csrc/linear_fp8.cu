@@ -17,6 +17,8 @@
 namespace gdr {
 namespace {
 
+constexpr int kSms = 148;
+
 // Set by a kernel that gave up a bounded wait; read and cleared by
 // gdr_linear_fp8_status.
 __device__ uint32_t g_linear_error;
@@ -95,7 +97,6 @@ __device__ __forceinline__ void st_async4(uint32_t cluster_dst, const float4& v,
 //   warp 5      TMEM allocation, MMAs
 // ---------------------------------------------------------------------------
 constexpr int kFewThreads = 192;
-constexpr int kFewRows = 64;
 
 template <int BN>
 struct FewLayout {
@@ -356,37 +357,47 @@ struct OutMaps {
     int valid[GDR_LINEAR_MAX_OUTS];
 };
 
-// One slot of outputs to global memory, by one warp: columns from c0 (128 of bf16,
-// 64 of fp32), rows row0 .. below M.  A block of columns inside one range goes by
-// two TMA stores (which drop what lies past the tensor's rows and columns), others
-// element by element, a lane per column.
-__device__ __forceinline__ void store_slot(const OutRanges& out, const OutMaps& maps, const uint8_t* slot, bool wide,
-                                           int c0, int row0, int M, int lane) {
+// The range that a slot of outputs goes to by TMA (columns from c0, 128 of bf16 or
+// 64 of fp32, all in one range with a map, at a 16-byte boundary of its rows), or
+// -1.  What lies past the last range's columns is dropped by the store.
+__device__ __forceinline__ int slot_range(const OutRanges& out, const OutMaps& maps, bool wide, int c0) {
     const int cols = wide ? 64 : 128, elem = wide ? 4 : 2;
     int r = 0;
     while (r + 1 < out.n_outs && c0 >= out.begin[r + 1]) ++r;
-    const int off = c0 - out.begin[r];
-    if ((c0 + cols <= out.begin[r + 1] || r + 1 == out.n_outs) && (out.f32[r] != 0) == wide && maps.valid[r] &&
-        (off * elem & 15) == 0) {
-        if (row0 < M && elect_one()) {
-            tma_store_2d(&maps.map[r], slot, off, row0);
-            if (c0 + cols / 2 < out.begin[r + 1]) tma_store_2d(&maps.map[r], slot + 16384, off + cols / 2, row0);
-            bulk_commit_group();
-            bulk_wait_group_read0();
-        }
-        __syncwarp();
-        return;
-    }
-    const int rows = M - row0 < 128 ? M - row0 : 128;
-    for (int q = lane; q < cols; q += 32) {
+    const bool ok = (c0 + cols <= out.begin[r + 1] || r + 1 == out.n_outs) && (out.f32[r] != 0) == wide && maps.valid[r] &&
+                    ((c0 - out.begin[r]) * elem & 15) == 0;
+    return ok ? r : -1;
+}
+
+// The other slots: a warp's 32 rows (from `first` of the CTA's 128), a lane per
+// column.
+__device__ __forceinline__ void store_rows(const OutRanges& out, const uint8_t* slot, bool wide, int c0, int row0,
+                                           int first, int M, int lane) {
+    const int rows = M - row0 - first < 32 ? M - row0 - first : 32;
+    const int elem = wide ? 4 : 2;
+    for (int q = lane; q < (wide ? 64 : 128); q += 32) {
         const OutColumn o(out, c0 + q);
         if (!o.pitch) continue;
         const int chunk = q * elem >> 4, in = q * elem & 15;
+        const uint8_t* at = slot + (chunk >> 3) * 16384 + first * 128 + in;
+        const int64_t pitch = o.pitch;
+        const int64_t start = (int64_t)(row0 + first) * pitch;
+        if (!wide) {
+            uint16_t* p = (uint16_t*)o.p + start;
 #pragma unroll 8
-        for (int j = 0; j < rows; ++j) {
-            const uint8_t* at = slot + slot_chunk(j, chunk) + in;
-            o.store(row0 + j, wide ? *reinterpret_cast<const float*>(at)
-                                   : __bfloat162float(*reinterpret_cast<const __nv_bfloat16*>(at)));
+            for (int j = 0; j < rows; ++j)
+                p[j * pitch] = *reinterpret_cast<const uint16_t*>(at + j * 128 + (((chunk & 7) ^ (j & 7)) << 4));
+        } else if (o.f32) {
+            float* p = (float*)o.p + start;
+#pragma unroll 8
+            for (int j = 0; j < rows; ++j)
+                p[j * pitch] = *reinterpret_cast<const float*>(at + j * 128 + (((chunk & 7) ^ (j & 7)) << 4));
+        } else {
+            __nv_bfloat16* p = (__nv_bfloat16*)o.p + start;
+#pragma unroll 8
+            for (int j = 0; j < rows; ++j)
+                p[j * pitch] = __float2bfloat16_rn(
+                    *reinterpret_cast<const float*>(at + j * 128 + (((chunk & 7) ^ (j & 7)) << 4)));
         }
     }
 }
@@ -501,10 +512,21 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_const
                 if (c0 >= N || !ok) break;
                 const bool wide = block_is_wide(out, c0, lane);
                 for (int q = 0; q < (wide ? 2 : 1); ++q) {
+                    const int c = c0 + q * 64, r = slot_range(out, maps, wide, c);
+                    if (r < 0) continue;                     // warps 0-7 store it
                     if (!warp_wait(&slot_full[half], jobs[half] & 1, &gave_up)) { ok = false; break; }
-                    store_slot(out, maps, smem + kPairStaging + half * kPairSlotBytes, wide, c0 + q * 64, row0, M, lane);
+                    if (elect_one()) {
+                        const int off = c - out.begin[r], box = wide ? 32 : 64;
+                        const uint8_t* slot = smem + kPairStaging + half * kPairSlotBytes;
+                        if (row0 < M) {
+                            tma_store_2d(&maps.map[r], slot, off, row0);
+                            if (c + box < out.begin[r + 1]) tma_store_2d(&maps.map[r], slot + 16384, off + box, row0);
+                        }
+                        bulk_commit_group();
+                        bulk_wait_group_read0();
+                        mbar_arrive(&slot_free[half]);
+                    }
                     __syncwarp();
-                    if (lane == 0) mbar_arrive(&slot_free[half]);
                     ++jobs[half];
                 }
             }
@@ -524,7 +546,7 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_const
         bool ok = true;
         // this tile's factor rows; the first four groups' factors are fetched a tile ahead
         const float *sxp = sx, *swp = sw;
-        int c0 = 0;
+        int c0 = 0, m0 = 0;
         float4 nx, nw;
         const auto fetch = [&](int g) {
             if (vec) {
@@ -541,7 +563,8 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_const
         const auto enter = [&](int t) {
             int tm, tn;
             pair_tile(t, tiles_m, tiles_n, &tm, &tn);
-            const int m = tm * 256 + (int)rank * 128 + row;
+            m0 = tm * 256 + (int)rank * 128;
+            const int m = m0 + row;
             c0 = tn * 256 + half * 128;
             sxp = sx + (int64_t)(m < M ? m : 0) * groups;
             swp = sw + (int64_t)(c0 < N ? tn * 2 + half : 0) * groups;
@@ -580,34 +603,39 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_const
                 __syncwarp();
                 if (lane == 0) mbar_arrive_cluster(buf ? bar1 : bar0);
             }
-            const int c_out = c0;
+            const int c_out = c0, m_tile = m0;
             if (t + pairs < tiles) enter(t + pairs);
             if (!ok || c_out >= N) continue;
-            if (block_is_wide(out, c_out, lane)) {
+            const bool wide = block_is_wide(out, c_out, lane);
 #pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    if (jobs > 0 && !warp_wait(&slot_free[half], (jobs - 1) & 1, &gave_up)) { ok = false; break; }
+            for (int h = 0; h < 2; ++h) {
+                if (h == 1 && !wide) break;
+                // the slot's last TMA store has read it
+                if (jobs > 0 && !warp_wait(&slot_free[half], (jobs - 1) & 1, &gave_up)) { ok = false; break; }
+                if (wide) {
 #pragma unroll
                     for (int c = 0; c < 16; ++c)
                         *reinterpret_cast<float4*>(slot + slot_chunk(row, c)) =
                             make_float4(acc[h * 32 + 2 * c].x, acc[h * 32 + 2 * c].y, acc[h * 32 + 2 * c + 1].x,
                                         acc[h * 32 + 2 * c + 1].y);
+                } else {
+#pragma unroll
+                    for (int c = 0; c < 16; ++c)
+                        *reinterpret_cast<uint4*>(slot + slot_chunk(row, c)) =
+                            make_uint4(pack_bf16(acc[4 * c].x, acc[4 * c].y), pack_bf16(acc[4 * c + 1].x, acc[4 * c + 1].y),
+                                       pack_bf16(acc[4 * c + 2].x, acc[4 * c + 2].y), pack_bf16(acc[4 * c + 3].x, acc[4 * c + 3].y));
+                }
+                const int c = c_out + h * 64;
+                if (slot_range(out, maps, wide, c) >= 0) {
                     fence_proxy_async_smem();
                     __syncwarp();
                     if (lane == 0) mbar_arrive(&slot_full[half]);
                     ++jobs;
+                } else {
+                    __syncwarp();
+                    store_rows(out, slot, wide, c, m_tile, (warp & 3) * 32, M, lane);
+                    __syncwarp();
                 }
-            } else {
-                if (jobs > 0 && !warp_wait(&slot_free[half], (jobs - 1) & 1, &gave_up)) { ok = false; continue; }
-#pragma unroll
-                for (int c = 0; c < 16; ++c)
-                    *reinterpret_cast<uint4*>(slot + slot_chunk(row, c)) =
-                        make_uint4(pack_bf16(acc[4 * c].x, acc[4 * c].y), pack_bf16(acc[4 * c + 1].x, acc[4 * c + 1].y),
-                                   pack_bf16(acc[4 * c + 2].x, acc[4 * c + 2].y), pack_bf16(acc[4 * c + 3].x, acc[4 * c + 3].y));
-                fence_proxy_async_smem();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&slot_full[half]);
-                ++jobs;
             }
         }
     }
@@ -702,9 +730,16 @@ cudaError_t launch_few(const gdr_linear_fp8_args& a, EncodeTiledFn enc, cudaStre
     const int groups = fp8_groups(a.k), tiles = fp8_groups(a.n);
     const int64_t token_tiles = (a.rows + BN - 1) / BN;
     if (token_tiles > 65535) return cudaErrorInvalidValue;
-    // as many parts of K (a power of two) as fill the SMs twice, none without work
+    // K in a power of two of parts, none without work: as many as fill the SMs once
+    // (4096 x 4096 for one token: 5.2 us, filled twice 6.3; the next kernel's start
+    // then overlaps this one), and twice where a CTA would have 16 groups or more of
+    // 64 tokens to add up (36 x 16416 x 4096: 17.0 against 19.1 us).
     int split = 1;
-    while (split < 8 && 2 * split <= groups && 2 * split * tiles * token_tiles <= 2 * 148) split *= 2;
+    while (split < 8 && 2 * split <= groups) {
+        const int64_t ctas = 2 * split * tiles * token_tiles;
+        if (ctas > kSms && !(BN == 64 && groups >= 32 * split && ctas <= 2 * kSms)) break;
+        split *= 2;
+    }
     if ((int64_t)tiles * split > (int64_t)INT32_MAX) return cudaErrorInvalidValue;
     CUtensorMap mw, mx;
     cudaError_t e;
@@ -731,7 +766,7 @@ cudaError_t launch_pair(const gdr_linear_fp8_args& a, EncodeTiledFn enc, cudaStr
         if ((e = out_map(enc, &maps.map[i], a.out[i], a.rows, a.out_cols[i], elem)) != cudaSuccess) return e;
         maps.valid[i] = 1;
     }
-    const int64_t pairs = tiles_m * tiles_n < 74 ? tiles_m * tiles_n : 74;
+    const int64_t pairs = tiles_m * tiles_n < kSms / 2 ? tiles_m * tiles_n : kSms / 2;
     return launch_cluster(linear_pair_kernel, dim3((unsigned)(2 * pairs)), dim3(kPairThreads), kPairDynBytes, 2, st,
                           mw, mx, a.x_scale, a.w_scale, (int)a.rows, a.n, groups, (int)tiles_m, (int)tiles_n,
                           out_ranges(a), maps);
@@ -745,7 +780,12 @@ cudaError_t launch_linear_fp8(const gdr_linear_fp8_args& a, cudaStream_t st) {
     if (e != cudaSuccess) return e;
     if (a.rows <= 16) return launch_few<16>(a, enc, st);
     if (a.rows <= 32) return launch_few<32>(a, enc, st);
-    if (a.rows <= kFewRows) return launch_few<64>(a, enc, st);
+    // Up to 64 tokens, and more while the tiles of 64 tokens x 128 columns fit the SMs
+    // at once (128 x 4096 x 4096: 11 us against 18 on 16 CTA pairs); beyond that every
+    // weight would be fetched again for each 64 tokens (256 x 16416 x 4096: 51 us
+    // against 22).
+    const int64_t small_tiles = fp8_groups(a.n) * ((a.rows + 63) / 64);
+    if (a.rows <= 64 || small_tiles <= kSms) return launch_few<64>(a, enc, st);
     return launch_pair(a, enc, st);
 }
 
