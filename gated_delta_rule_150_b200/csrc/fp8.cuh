@@ -24,7 +24,7 @@ struct Octet<__nv_bfloat16> {
     __device__ __forceinline__ void load(const __nv_bfloat16* p) {
         raw = __ldcs(reinterpret_cast<const uint4*>(p));
     }
-    __device__ __forceinline__ void to_float(float (&f)[8]) const {
+    __device__ __forceinline__ void to_float(float* f) const {
         const uint32_t u[4] = {raw.x, raw.y, raw.z, raw.w};
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
@@ -51,7 +51,7 @@ struct Octet<float> {
         lo = __ldcs(reinterpret_cast<const float4*>(p));
         hi = __ldcs(reinterpret_cast<const float4*>(p) + 1);
     }
-    __device__ __forceinline__ void to_float(float (&f)[8]) const {
+    __device__ __forceinline__ void to_float(float* f) const {
         f[0] = lo.x; f[1] = lo.y; f[2] = lo.z; f[3] = lo.w;
         f[4] = hi.x; f[5] = hi.y; f[6] = hi.z; f[7] = hi.w;
     }
@@ -64,17 +64,19 @@ struct Octet<float> {
 // max |f| as its bit pattern: ordered like the values, infinity above every
 // finite value and NaN above infinity, so a maximum of patterns keeps a NaN
 // (fmaxf would drop it).
-__device__ __forceinline__ uint32_t abs_bits_max(const float (&f)[8]) {
+template <int N>
+__device__ __forceinline__ uint32_t abs_bits_max(const float (&f)[N]) {
     uint32_t m = 0u;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) m = max(m, __float_as_uint(f[i]) & 0x7fffffffu);
+    for (int i = 0; i < N; ++i) m = max(m, __float_as_uint(f[i]) & 0x7fffffffu);
     return m;
 }
 
-// Maximum over the 16 lanes (an aligned half warp) that hold one group.
-__device__ __forceinline__ uint32_t half_warp_max(uint32_t m) {
+// Maximum over the aligned LANES lanes that hold one group.
+template <int LANES>
+__device__ __forceinline__ uint32_t lanes_max(uint32_t m) {
 #pragma unroll
-    for (int s = 8; s > 0; s >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, s));
+    for (int s = LANES / 2; s > 0; s >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, s));
     return m;
 }
 
@@ -83,9 +85,13 @@ __device__ __forceinline__ float fp8_scale(uint32_t amax_bits) {
     return (a < 1e-12f ? 1e-12f : a) / 448.f;      // a NaN stays
 }
 
-// Codes of an octet: y * (1 / scale), saturating (a rounding of 1 / scale may
-// lift the largest value an fp32 step above 448).
-__device__ __forceinline__ uint2 fp8_codes(const float (&y)[8], float inv_scale) {
+// 1 / scale to 2 ulp (a scale lies between 2e-15 and 8e35, where the approximate
+// division is good; 0 for an infinite one, NaN stays).
+__device__ __forceinline__ float fp8_inverse(float scale) { return __fdividef(1.f, scale); }
+
+// Codes of eight values: y * (1 / scale), saturating (the rounding of 1 / scale
+// may lift the largest value a few fp32 steps above 448).
+__device__ __forceinline__ uint2 fp8_codes(const float* y, float inv_scale) {
     uint32_t h[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i)

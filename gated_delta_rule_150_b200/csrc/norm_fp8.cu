@@ -5,9 +5,7 @@
 // All three read every input once and write every output once: a row (or a
 // group, or a 128 x 128 block) stays in registers from its load to its codes.
 // They are bound by HBM.  A thread holds octets (eight consecutive channels,
-// one 16-byte load of bf16); octet j of a row belongs to the row's group j / 16,
-// so an aligned half warp holds exactly one group and finds its maximum by four
-// shuffles.
+// one 16-byte load of bf16).
 #include "fp8.cuh"
 #include "internal.h"
 #include "sm100.cuh"
@@ -17,20 +15,22 @@ namespace {
 
 // ---------------------------------------------------------------------------
 // y = h / sqrt(mean h^2 + eps) * w with h = x + residual.
-// TPR threads own a row (a warp, or a whole CTA), each up to IT octets of it,
-// kept in registers as fp32 between the sum of squares and the codes.
+// A row belongs to a warp (ROWS = 4 rows per CTA, up to 64 octets) or to a whole
+// CTA (ROWS = 1), each thread with up to IT octets of it, kept in registers as
+// fp32 between the sum of squares and the codes.  Octet j of a row belongs to the
+// row's group j / 16, so an aligned half warp holds exactly one group.
 // ---------------------------------------------------------------------------
-template <typename T, bool RES, int TPR, int IT>
-__global__ void __launch_bounds__(TPR < 128 ? 128 : TPR)
+template <typename T, bool RES, int ROWS, int IT>
+__global__ void __launch_bounds__(ROWS > 1 ? 32 * ROWS : IT > 2 ? 512 : 1024)
 norm_fp8_kernel(int rows, int width, const T* x, const T* residual, const float* __restrict__ weight,
                 float eps, T* residual_out, uint8_t* __restrict__ y, float* __restrict__ y_scale) {
-    constexpr int kWarps = TPR / 32;
-    __shared__ float part[kWarps];
+    __shared__ float part[32];
     pdl_wait();
     pdl_launch_dependents();
-    const int t = threadIdx.x % TPR;
-    const int row = blockIdx.x * (blockDim.x / TPR) + threadIdx.x / TPR;
-    if (TPR == 32 && row >= rows) return;          // whole warps; with TPR > 32 the grid is exact
+    const int TPR = ROWS > 1 ? 32 : blockDim.x;
+    const int t = ROWS > 1 ? threadIdx.x & 31 : threadIdx.x;
+    const int row = ROWS > 1 ? blockIdx.x * ROWS + (threadIdx.x >> 5) : blockIdx.x;
+    if (ROWS > 1 && row >= rows) return;           // whole warps
     const int n8 = width >> 3;
     const int64_t base = (int64_t)row * width;
     Octet<T> a[IT], b[IT];
@@ -67,12 +67,12 @@ norm_fp8_kernel(int rows, int width, const T* x, const T* residual, const float*
     }
 #pragma unroll
     for (int s = 16; s > 0; s >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, s);
-    if (kWarps > 1) {
+    if (ROWS == 1) {
         if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = ss;
         __syncthreads();
         ss = 0.f;
-#pragma unroll
-        for (int w = 0; w < kWarps; ++w) ss += part[w];
+        const int warps = blockDim.x >> 5;
+        for (int w = 0; w < warps; ++w) ss += part[w];
     }
     const float inv = rsqrtf(ss / (float)width + eps);
     const int groups = (width + kFp8Group - 1) / kFp8Group;
@@ -90,9 +90,9 @@ norm_fp8_kernel(int rows, int width, const T* x, const T* residual, const float*
 #pragma unroll
             for (int c = 0; c < 8; ++c) h[i][c] = 0.f;      // past the row: 0 * inv may be NaN
         }
-        const float s = fp8_scale(half_warp_max(abs_bits_max(h[i])));
+        const float s = fp8_scale(lanes_max<16>(abs_bits_max(h[i])));
         if (j < n8) {
-            *reinterpret_cast<uint2*>(y + base + 8 * j) = fp8_codes(h[i], 1.f / s);
+            *reinterpret_cast<uint2*>(y + base + 8 * j) = fp8_codes(h[i], fp8_inverse(s));
             if ((j & 15) == 0) y_scale[(int64_t)row * groups + (j >> 4)] = s;
         }
     }
@@ -100,65 +100,70 @@ norm_fp8_kernel(int rows, int width, const T* x, const T* residual, const float*
 
 // ---------------------------------------------------------------------------
 // y = o / sqrt(mean_d o^2 + eps) * w * sigmoid(gate), per head of D channels.
-// A half warp owns one group of 128 channels of a token (one head at D 128, two
-// at D 64); each thread works on U groups at once, a grid stride apart, so that
-// the loads of all of them are in flight together.
+// Eight lanes own one group of 128 channels of a token (one head at D 128, two at
+// D 64), 16 channels each: half the shuffles and divisions per channel of eight
+// channels a lane.
 // ---------------------------------------------------------------------------
 constexpr int kGatedThreads = 256;
 
-template <typename TO, typename TG, int D, int U>
+template <typename TO, typename TG, int D>
 __global__ void __launch_bounds__(kGatedThreads)
-gated_norm_fp8_kernel(int64_t tasks, int groups, int n8, const TO* __restrict__ o,
+gated_norm_fp8_kernel(int64_t tasks, int groups, int n16, const TO* __restrict__ o,
                       const TG* __restrict__ gate, const float* __restrict__ weight, float eps,
                       uint8_t* __restrict__ y, float* __restrict__ y_scale) {
     pdl_wait();
     pdl_launch_dependents();
-    const int lane = threadIdx.x & 15;
-    const int64_t first = ((int64_t)blockIdx.x * kGatedThreads + threadIdx.x) >> 4;
-    const int64_t stride = (int64_t)gridDim.x * (kGatedThreads / 16);
-    float w[8];
-    {
-        const int c = (lane * 8) % D;
-        const float4 w0 = __ldg(reinterpret_cast<const float4*>(weight + c));
-        const float4 w1 = __ldg(reinterpret_cast<const float4*>(weight + c) + 1);
-        w[0] = w0.x; w[1] = w0.y; w[2] = w0.z; w[3] = w0.w;
-        w[4] = w1.x; w[5] = w1.y; w[6] = w1.z; w[7] = w1.w;
-    }
-    Octet<TO> a[U];
-    Octet<TG> b[U];
-    int64_t at[U];                                   // first channel of the octet, -1: none
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-        const int64_t task = first + u * stride;
+    const int lane = threadIdx.x & 7;
+    const int64_t task = ((int64_t)blockIdx.x * kGatedThreads + threadIdx.x) >> 3;
+    int64_t at = -1;                                 // first of this thread's 16 channels, -1: none
+    if (n16 == groups * 8) {                         // no shorter last group: groups lie end to end
+        if (task < tasks) at = (task * 8 + lane) * 16;
+    } else {
         const int64_t row = task / groups;
-        const int j = (int)(task - row * groups) * 16 + lane;
-        at[u] = task < tasks && j < n8 ? (row * n8 + j) * 8 : -1;
+        const int j = (int)(task - row * groups) * 8 + lane;
+        if (task < tasks && j < n16) at = (row * n16 + j) * 16;
+    }
+    Octet<TO> a[2];
+    Octet<TG> b[2];
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
         a[u].zero();
         b[u].zero();
-        if (at[u] >= 0) {
-            a[u].load(o + at[u]);
-            b[u].load(gate + at[u]);
+        if (at >= 0) {
+            a[u].load(o + at + 8 * u);
+            b[u].load(gate + at + 8 * u);
         }
     }
+    float f[16];
+    a[0].to_float(f);
+    a[1].to_float(f + 8);
+    float ss = 0.f;
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-        float f[8], g[8];
-        a[u].to_float(f);
+    for (int c = 0; c < 16; ++c) ss = fmaf(f[c], f[c], ss);
+#pragma unroll
+    for (int s = D / 32; s > 0; s >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, s);
+    const float inv = rsqrtf(ss * (1.f / D) + eps);
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+        float g[8];
         b[u].to_float(g);
-        float ss = 0.f;
 #pragma unroll
-        for (int c = 0; c < 8; ++c) ss = fmaf(f[c], f[c], ss);
+        for (int h = 0; h < 2; ++h) {
+            const float4 w = __ldg(reinterpret_cast<const float4*>(weight + (lane * 16) % D) + 2 * u + h);
+            const float wc[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
-        for (int s = D / 16; s > 0; s >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, s);
-        const float inv = rsqrtf(ss * (1.f / D) + eps);
-#pragma unroll
-        for (int c = 0; c < 8; ++c)
-            f[c] = at[u] >= 0 ? __fdividef(f[c] * inv * w[c], 1.f + __expf(-g[c])) : 0.f;
-        const float s = fp8_scale(half_warp_max(abs_bits_max(f)));
-        if (at[u] >= 0) {
-            *reinterpret_cast<uint2*>(y + at[u]) = fp8_codes(f, 1.f / s);
-            if (lane == 0) y_scale[first + u * stride] = s;
+            for (int c = 0; c < 4; ++c) {
+                float& v = f[8 * u + 4 * h + c];
+                v = at >= 0 ? __fdividef(v * inv * wc[c], 1.f + __expf(-g[4 * h + c])) : 0.f;
+            }
         }
+    }
+    const float s = fp8_scale(lanes_max<8>(abs_bits_max(f)));
+    if (at >= 0) {
+        const float si = fp8_inverse(s);
+        const uint2 lo = fp8_codes(f, si), hi = fp8_codes(f + 8, si);
+        *reinterpret_cast<uint4*>(y + at) = make_uint4(lo.x, lo.y, hi.x, hi.y);
+        if (lane == 0) y_scale[task] = s;
     }
 }
 
@@ -196,7 +201,7 @@ quantize_weight_kernel(int n, int k, int k_groups, const T* __restrict__ w, uint
     __syncthreads();
 #pragma unroll
     for (int i = 0; i < kQuantThreads / 32; ++i) m = max(m, part[i]);
-    const float s = fp8_scale(m), inv = 1.f / s;
+    const float s = fp8_scale(m), inv = fp8_inverse(s);
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
         const int row = row0 + 16 * i;
@@ -208,37 +213,39 @@ quantize_weight_kernel(int n, int k, int k_groups, const T* __restrict__ w, uint
     if (threadIdx.x == 0) scales[blockIdx.x] = s;
 }
 
-template <typename T, bool RES, int TPR, int IT>
-cudaError_t launch_norm_shape(const gdr_norm_fp8_args& a, cudaStream_t st) {
-    constexpr int threads = TPR < 128 ? 128 : TPR;
-    constexpr int rows_per_cta = threads / TPR;
-    const unsigned grid = (unsigned)((a.rows + rows_per_cta - 1) / rows_per_cta);
-    return launch_pdl(true, norm_fp8_kernel<T, RES, TPR, IT>, dim3(grid), dim3(threads), 0, st,
-                      (int)a.rows, a.width, (const T*)a.x, (const T*)a.residual, a.norm_weight,
-                      a.norm_eps, (T*)a.residual_out, (uint8_t*)a.y, a.y_scale);
+template <typename T, bool RES, int ROWS, int IT>
+cudaError_t launch_norm_shape(const gdr_norm_fp8_args& a, int threads, cudaStream_t st) {
+    const unsigned grid = (unsigned)((a.rows + ROWS - 1) / ROWS);
+    return launch_pdl(true, norm_fp8_kernel<T, RES, ROWS, IT>, dim3(grid), dim3(threads), 0, st, (int)a.rows,
+                      a.width, (const T*)a.x, (const T*)a.residual, a.norm_weight, a.norm_eps,
+                      (T*)a.residual_out, (uint8_t*)a.y, a.y_scale);
 }
 
+// Two octets a thread: 8192 rows of 896 take 10.4 us with 64 threads a row, 11.5
+// with one warp of four octets, 11.3 with 128 of one; 65536 rows of 2048 take 139
+// us with 128 threads, 145 with a warp, 157 with 256.  With too few rows to fill
+// the SMs one octet a thread (a single row of 896: 2.2 against 2.4 us).
 template <typename T, bool RES>
 cudaError_t launch_norm_typed(const gdr_norm_fp8_args& a, cudaStream_t st) {
     const int n8 = a.width / 8;
-    if (n8 <= 32 * 4) return launch_norm_shape<T, RES, 32, 4>(a, st);
-    if (n8 <= 128 * 4) return launch_norm_shape<T, RES, 128, 4>(a, st);
-    if (n8 <= 512 * 2) return launch_norm_shape<T, RES, 512, 2>(a, st);
-    return launch_norm_shape<T, RES, 512, 8>(a, st);
+    const auto warps = [n8](int it) { return 32 * ((n8 + 32 * it - 1) / (32 * it)); };
+    if (a.rows <= 2 * 148 && n8 <= 1024) return launch_norm_shape<T, RES, 1, 1>(a, warps(1), st);
+    if (n8 <= 64) return launch_norm_shape<T, RES, 4, 2>(a, 128, st);
+    if (n8 <= 2048) return launch_norm_shape<T, RES, 1, 2>(a, warps(2), st);
+    return launch_norm_shape<T, RES, 1, 8>(a, warps(8), st);
 }
 
 template <typename TO, typename TG>
 cudaError_t launch_gated_typed(const gdr_gated_norm_fp8_args& a, cudaStream_t st) {
-    constexpr int U = 2;
     const int width = a.n_heads * a.d_v;
     const int groups = fp8_groups(width);
     const int64_t tasks = a.rows * groups;
-    constexpr int64_t per_cta = kGatedThreads / 16 * U;
+    constexpr int64_t per_cta = kGatedThreads / 8;
     const int64_t grid = (tasks + per_cta - 1) / per_cta;
     if (grid > (int64_t)INT32_MAX) return cudaErrorInvalidValue;
-    auto kern = a.d_v == 64 ? gated_norm_fp8_kernel<TO, TG, 64, U> : gated_norm_fp8_kernel<TO, TG, 128, U>;
+    auto kern = a.d_v == 64 ? gated_norm_fp8_kernel<TO, TG, 64> : gated_norm_fp8_kernel<TO, TG, 128>;
     return launch_pdl(true, kern, dim3((unsigned)grid), dim3(kGatedThreads), 0, st, tasks, groups,
-                      width / 8, (const TO*)a.o, (const TG*)a.gate_raw, a.norm_weight, a.norm_eps,
+                      width / 16, (const TO*)a.o, (const TG*)a.gate_raw, a.norm_weight, a.norm_eps,
                       (uint8_t*)a.y, a.y_scale);
 }
 
