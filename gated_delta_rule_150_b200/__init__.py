@@ -772,11 +772,15 @@ def _groups(width: int) -> int:
     return -(-width // FP8_GROUP)
 
 
-def _need_same_device(*ts):
-    """One launch reads and writes all of them."""
+def _need_one_device(*ts):
+    """CUDA tensors, contiguous, all on one device: one launch reads and writes them."""
     dev = None
     for t in ts:
         if t is not None:
+            if not t.is_cuda:
+                raise ValueError("all tensors must be CUDA tensors")
+            if not t.is_contiguous():
+                raise ValueError("all tensors must be contiguous")
             if dev is None:
                 dev = t.device
             elif t.device != dev:
@@ -809,6 +813,20 @@ def _check_eps(norm_eps):
         raise ValueError("norm_eps must be >= 0 and finite")
 
 
+# The current stream as an integer (torch.cuda.current_stream builds an object for
+# it, which takes a third of a small call's time on the host).
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
+    (lambda index: torch.cuda.current_stream(index).cuda_stream)
+
+
+def _on_device(index, fn, *args, stream=None):
+    """fn(*args, stream) with device ``index`` current (its current stream by default)."""
+    if torch.cuda.current_device() == index:
+        return fn(*args, _raw_stream(index) if stream is None else stream)
+    with torch.cuda.device(index):
+        return fn(*args, _raw_stream(index) if stream is None else stream)
+
+
 class _Prepared:
     """One library call whose argument block is built and checked once and
     replayed.  Holds references to every tensor it points at.  ``run()`` enqueues
@@ -825,14 +843,8 @@ class _Prepared:
         self._ref = ctypes.byref(args)
 
     def run(self, stream=None):
-        if torch.cuda.current_device() != self._index:
-            with torch.cuda.device(self._index):
-                return self._call(stream)
-        return self._call(stream)
-
-    def _call(self, stream):
-        st = stream if stream is not None else torch.cuda.current_stream(self._index)
-        status = self._fn(self._ref, st.cuda_stream)
+        status = _on_device(self._index, self._fn, self._ref,
+                            stream=None if stream is None else stream.cuda_stream)
         if status != GDR_OK:
             raise GdrError(status, self._what)
         return self.outputs
@@ -858,9 +870,9 @@ class PreparedNormFp8(_Prepared):
         _expect(out, (rows, width), torch.float8_e4m3fn, "out")
         _expect(out_scale, (rows, _groups(width)), torch.float32, "out_scale")
         _check_eps(norm_eps)
-        _need_cuda(x, norm_weight, residual, out, out_scale, residual_out)
-        _need_same_device(x, norm_weight, residual, out, out_scale, residual_out)
+        _need_one_device(x, norm_weight, residual, out, out_scale, residual_out)
         dev = x.device
+        given = not (out is None and out_scale is None and residual_out is None)
         if out is None:
             out = torch.empty(rows, width, dtype=torch.float8_e4m3fn, device=dev)
         if out_scale is None:
@@ -869,9 +881,10 @@ class PreparedNormFp8(_Prepared):
             residual_out = torch.empty_like(x)
         _need_aligned16(x=x, norm_weight=norm_weight, residual=residual, residual_out=residual_out,
                         out=out)
-        _need_apart([("residual_out", residual_out), ("out", out), ("out_scale", out_scale)],
-                    [("x", x), ("residual", residual), ("norm_weight", norm_weight)],
-                    same={("residual_out", "x"), ("residual_out", "residual")})
+        if given:
+            _need_apart([("residual_out", residual_out), ("out", out), ("out_scale", out_scale)],
+                        [("x", x), ("residual", residual), ("norm_weight", norm_weight)],
+                        same={("residual_out", "x"), ("residual_out", "residual")})
         a = NormFp8Args()
         a.rows, a.width, a.io_dtype = rows, width, dtype
         a.x, a.norm_weight, a.norm_eps = x.data_ptr(), norm_weight.data_ptr(), float(norm_eps)
@@ -916,15 +929,16 @@ class PreparedGatedNormFp8(_Prepared):
         a = GatedNormFp8Args()
         a.rows, a.n_heads, a.d_v = rows, H, d
         a.o_dtype, a.gate_dtype = _dtype_code(o), _dtype_code(gate_raw)
-        _need_cuda(o, gate_raw, norm_weight, out, out_scale)
-        _need_same_device(o, gate_raw, norm_weight, out, out_scale)
+        _need_one_device(o, gate_raw, norm_weight, out, out_scale)
+        given = not (out is None and out_scale is None)
         if out is None:
             out = torch.empty(rows, H * d, dtype=torch.float8_e4m3fn, device=o.device)
         if out_scale is None:
             out_scale = torch.empty(rows, _groups(H * d), dtype=torch.float32, device=o.device)
         _need_aligned16(o=o, gate_raw=gate_raw, norm_weight=norm_weight, out=out)
-        _need_apart([("out", out), ("out_scale", out_scale)],
-                    [("o", o), ("gate_raw", gate_raw), ("norm_weight", norm_weight)])
+        if given:
+            _need_apart([("out", out), ("out_scale", out_scale)],
+                        [("o", o), ("gate_raw", gate_raw), ("norm_weight", norm_weight)])
         a.o, a.gate_raw, a.norm_weight = o.data_ptr(), gate_raw.data_ptr(), norm_weight.data_ptr()
         a.norm_eps = float(norm_eps)
         a.y, a.y_scale = out.data_ptr(), out_scale.data_ptr()
@@ -953,17 +967,18 @@ def quantize_weight_fp8(w, *, out=None, out_scale=None):
         raise ValueError(f"K must be a positive multiple of 16, got {k}")
     _expect(out, (n, k), torch.float8_e4m3fn, "out")
     _expect(out_scale, (_groups(n), _groups(k)), torch.float32, "out_scale")
-    _need_cuda(w, out, out_scale)
-    _need_same_device(w, out, out_scale)
+    _need_one_device(w, out, out_scale)
+    given = not (out is None and out_scale is None)
+    dev = w.device
     if out is None:
-        out = torch.empty(n, k, dtype=torch.float8_e4m3fn, device=w.device)
+        out = torch.empty(n, k, dtype=torch.float8_e4m3fn, device=dev)
     if out_scale is None:
-        out_scale = torch.empty(_groups(n), _groups(k), dtype=torch.float32, device=w.device)
+        out_scale = torch.empty(_groups(n), _groups(k), dtype=torch.float32, device=dev)
     _need_aligned16(w=w, out=out)
-    _need_apart([("out", out), ("out_scale", out_scale)], [("w", w)])
-    with torch.cuda.device(w.device):
-        _check(lib().gdr_quantize_weight_fp8(n, k, dtype, _ptr(w), _ptr(out), _ptr(out_scale),
-                                             _stream(w.device)), "gdr_quantize_weight_fp8")
+    if given:
+        _need_apart([("out", out), ("out_scale", out_scale)], [("w", w)])
+    _check(_on_device(dev.index, lib().gdr_quantize_weight_fp8, n, k, dtype, w.data_ptr(),
+                      out.data_ptr(), out_scale.data_ptr()), "gdr_quantize_weight_fp8")
     return out, out_scale
 
 
@@ -996,13 +1011,14 @@ class PreparedLinearFp8(_Prepared):
             raise ValueError("out must hold one tensor for each split")
         for i, t in enumerate(outs):
             _expect(t, (rows, cols[i]), dtypes[i], f"out[{i}]")
-        _need_cuda(x, x_scale, w, w_scale, *outs)
-        _need_same_device(x, x_scale, w, w_scale, *outs)
+        _need_one_device(x, x_scale, w, w_scale, *outs)
+        given = any(t is not None for t in outs)
         outs = [torch.empty(rows, c, dtype=t, device=x.device) if o is None else o
                 for o, c, t in zip(outs, cols, dtypes)]
         _need_aligned16(x=x, w=w)
-        _need_apart([(f"out[{i}]", t) for i, t in enumerate(outs)],
-                    [("x", x), ("x_scale", x_scale), ("w", w), ("w_scale", w_scale)])
+        if given:
+            _need_apart([(f"out[{i}]", t) for i, t in enumerate(outs)],
+                        [("x", x), ("x_scale", x_scale), ("w", w), ("w_scale", w_scale)])
         a = LinearFp8Args()
         a.rows, a.n, a.k = rows, n, k
         a.x, a.x_scale, a.w, a.w_scale = (x.data_ptr(), x_scale.data_ptr(), w.data_ptr(),
