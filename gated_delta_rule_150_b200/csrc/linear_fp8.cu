@@ -102,6 +102,7 @@ __device__ __forceinline__ void st_async4(uint32_t cluster_dst, const float4& v,
 //   warp 5      TMEM allocation, MMAs
 // ---------------------------------------------------------------------------
 constexpr int kFewThreads = 192;
+constexpr int kFewAccs = 4;             // TMEM accumulators: groups between an MMA and its sums
 
 template <int BN>
 struct FewLayout {
@@ -113,7 +114,7 @@ struct FewLayout {
     static constexpr uint32_t kFactors = kParts + (kGroups < 8 ? 8 : kGroups) * kPartBytes;
     static constexpr uint32_t kBytes = kFactors + 4u * 2u * BN * 4u;    // 4 warps x 2 x BN floats
     static constexpr uint32_t kDynBytes = kBytes + 1024u;               // 1024-byte alignment
-    static constexpr uint32_t kTmemCols = 2 * BN < 32 ? 32 : 2 * BN;
+    static constexpr uint32_t kTmemCols = kFewAccs * BN;
 };
 
 template <int BN>
@@ -125,7 +126,7 @@ linear_few_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_consta
     constexpr int ST = Lay::kStages;
     extern __shared__ uint8_t dyn[];
     uint8_t* smem = align_smem<1024>(dyn);
-    __shared__ uint64_t full[ST], empty[ST], acc_full[2], acc_empty[2], drained, parts_bar;
+    __shared__ uint64_t full[ST], empty[ST], acc_full[kFewAccs], acc_empty[kFewAccs], drained, parts_bar;
     __shared__ uint32_t tmem_slot;
     __shared__ int gave_up;
     const int warp = warp_index(), lane = threadIdx.x & 31;
@@ -139,7 +140,7 @@ linear_few_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_consta
 
     if (threadIdx.x == 0) {
         for (int i = 0; i < ST; ++i) { mbar_init(&full[i], 1); mbar_init(&empty[i], 1); }
-        for (int i = 0; i < 2; ++i) { mbar_init(&acc_full[i], 1); mbar_init(&acc_empty[i], 4); }
+        for (int i = 0; i < kFewAccs; ++i) { mbar_init(&acc_full[i], 1); mbar_init(&acc_empty[i], 4); }
         mbar_init(&drained, 1);
         mbar_init(&parts_bar, 1);
         gave_up = 0;
@@ -180,9 +181,9 @@ linear_few_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_consta
         constexpr uint32_t idesc = idesc_e4m3_f32(128, BN);
         bool ok = true;
         for (int i = 0, s = 0, phase = 0; i < count; ++i) {
-            const int buf = i & 1;
+            const int buf = i % kFewAccs;
             if (!warp_wait(&full[s], phase, &gave_up) ||
-                (i >= 2 && !warp_wait(&acc_empty[buf], ((i >> 1) & 1) ^ 1, &gave_up))) { ok = false; break; }
+                (i >= kFewAccs && !warp_wait(&acc_empty[buf], ((i / kFewAccs) & 1) ^ 1, &gave_up))) { ok = false; break; }
             tc_fence_after_sync();
             if (elect_one()) {
                 const uint32_t a = smem_u32(smem + s * Lay::kStageBytes);
@@ -223,14 +224,14 @@ linear_few_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_consta
         fetch(g0);
         bool ok = true;
         for (int i = 0; i < count; ++i) {
-            const int buf = i & 1;
-            float* f = factors + buf * BN;
+            const int buf = i % kFewAccs;
+            float* f = factors + (i & 1) * BN;
 #pragma unroll
             for (int p = 0; p < kPer; ++p)
                 if (BN >= 32 || lane < BN) f[p * 32 + lane] = next[p];
             if (i + 1 < count) fetch(g0 + i + 1);
             __syncwarp();
-            if (!warp_wait(&acc_full[buf], (i >> 1) & 1, &gave_up)) { ok = false; break; }
+            if (!warp_wait(&acc_full[buf], (i / kFewAccs) & 1, &gave_up)) { ok = false; break; }
             tc_fence_after_sync();
             const uint32_t at = tmem + ((uint32_t)(warp * 32) << 16) + buf * BN;
             float d[BN / kLoad][kLoad];
