@@ -303,31 +303,45 @@ linear_few_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_consta
 }
 
 // ---------------------------------------------------------------------------
-// Many tokens: CTA pairs on tiles of 256 tokens x 256 columns.  Each CTA loads
-// 128 tokens and 128 columns per K group (32 KB; two single CTAs on 128 x 256
-// tiles would pull 96 KB through L2), holds its 128 tokens x 256 columns in TMEM,
-// twice, and adds each finished group into registers with its factor.
-//   warps 0-7   a thread owns a token (row) and one half of the tile's columns,
-//               which is one weight block: a group's factor sx sw is one number
-//               per thread
+// Many tokens: CTA pairs on tiles of 256 tokens x NT columns.  Each CTA loads
+// 128 tokens and half of the columns per K group (32 KB at NT 256; two single CTAs
+// on 128 x 256 tiles would pull 96 KB through L2), holds its 128 tokens x NT columns
+// in TMEM, 512 / NT times, and adds each finished group into registers with its
+// factor.
+//   warps 0-7   a thread owns a token (row) and one half of the tile's columns, which
+//               lie in one weight block: a group's factor sx sw is one number per
+//               thread
 //   warp 8      TMA loads
-//   warps 9, 10 (even CTA) the MMAs of one half each
+//   warps 9, 10 (even CTA) the MMAs: of one half each at NT 256, of every other group
+//               at NT 128
 //   warp 11     stores the outputs that warps 0-7 leave in shared memory, while
 //               they are at the next tile
-// A half of a group's accumulator has its own barriers and its own issuing warp:
-// the way from an MMA's end through the register sums to the next MMA into the
-// same columns (commit, sums, arrival at the even CTA: about 750 cycles) then has
-// to fit into the other three quarters of TMEM (768 cycles of MMA), not into one
-// half of it (512).  Persistent: a pair takes tiles a grid stride apart.
+// The way from an MMA's end through the register sums to the next MMA into the same
+// columns (commit, sums, arrival at the even CTA: about 750 cycles) has to fit into
+// the MMA time of the rest of TMEM.  At NT 256 (two accumulators) it bounds the
+// kernel; each half of an accumulator has its own barriers and issuing warp there, so
+// that a half waits for itself only (8192 x 4096 x 4096: 114 us, whole accumulators
+// 117).  At NT 128 (four) the 24 KB a group that a CTA takes in at about 61 bytes a
+// cycle do.  NT 128 is for products whose tiles do not fill the SMs (512 x 4096 x
+// 4096: 13.3 us against 17.4; 8192 x 4096 x 4096: 139 against 114).  Long runs are
+// held at 1.3 GHz by the power limit.  Persistent: a pair takes tiles a grid stride
+// apart.
 // ---------------------------------------------------------------------------
 constexpr int kPairThreads = 384;
-constexpr int kPairStages = 5;
-constexpr uint32_t kPairStageBytes = 32768u;                 // 128 tokens, then 64 columns of either half
-constexpr uint32_t kPairStaging = kPairStages * kPairStageBytes;
-constexpr uint32_t kPairSlotBytes = 32768u;                  // 128 rows x 256 bytes of outputs, per half
-constexpr uint32_t kPairBytes = kPairStaging + 2u * kPairSlotBytes;
-constexpr uint32_t kPairDynBytes = kPairBytes + 1024u;
 constexpr int kPairRowGroup = 8;                             // token tiles that take their column tiles together
+
+template <int NT>
+struct PairLayout {
+    static constexpr bool kSplit = NT == 256;                // an issuing warp per half
+    static constexpr int kHalf = NT / 2;                     // columns of a CTA's loads and of an adder's sums
+    static constexpr int kAccs = 512 / NT;                   // TMEM accumulators, of two halves each
+    static constexpr int kStages = NT == 256 ? 5 : 6;
+    static constexpr uint32_t kStageBytes = 16384u + kHalf * 128u;
+    static constexpr uint32_t kSlots = kStages * kStageBytes;
+    static constexpr uint32_t kSlotBytes = 32768u;           // 128 rows x 256 bytes of outputs, per half
+    static constexpr uint32_t kBytes = kSlots + 2u * kSlotBytes;
+    static constexpr uint32_t kDynBytes = kBytes + 1024u;
+};
 
 // acc += f * v, two columns per instruction.
 template <int N>
@@ -347,12 +361,11 @@ __device__ __forceinline__ void pair_tile(int t, int tiles_m, int tiles_n, int* 
     *tm = first + (r - *tn * rows);
 }
 
-// Whether any of the columns c0 .. c0 + 127 below N goes to an fp32 tensor: their
-// outputs then pass through shared memory as fp32 (64 columns at a time),
-// otherwise as bf16 (128 at a time).
-__device__ __forceinline__ bool block_is_wide(const OutRanges& out, int c0, int lane) {
+// Whether any of the `cols` columns from c0 on goes to an fp32 tensor: their outputs
+// then pass through shared memory as fp32 (64 columns at a time), otherwise as bf16.
+__device__ __forceinline__ bool block_is_wide(const OutRanges& out, int c0, int cols, int lane) {
     bool wide = false;
-    if (lane < out.n_outs) wide = out.f32[lane] && out.begin[lane] < c0 + 128 && out.begin[lane + 1] > c0;
+    if (lane < out.n_outs) wide = out.f32[lane] && out.begin[lane] < c0 + cols && out.begin[lane + 1] > c0;
     return __any_sync(0xffffffffu, wide);
 }
 
@@ -370,11 +383,11 @@ struct OutMaps {
     int valid[GDR_LINEAR_MAX_OUTS];
 };
 
-// The range that a slot of outputs goes to by TMA (columns from c0, 128 of bf16 or
-// 64 of fp32, all in one range with a map, at a 16-byte boundary of its rows), or
-// -1.  What lies past the last range's columns is dropped by the store.
-__device__ __forceinline__ int slot_range(const OutRanges& out, const OutMaps& maps, bool wide, int c0) {
-    const int cols = wide ? 64 : 128, elem = wide ? 4 : 2;
+// The range that a slot of outputs goes to by TMA (`cols` columns from c0, all in one
+// range with a map, at a 16-byte boundary of its rows), or -1.  What lies past the
+// last range's columns is dropped by the store.
+__device__ __forceinline__ int slot_range(const OutRanges& out, const OutMaps& maps, bool wide, int c0, int cols) {
+    const int elem = wide ? 4 : 2;
     int r = 0;
     while (r + 1 < out.n_outs && c0 >= out.begin[r + 1]) ++r;
     const bool ok = (c0 + cols <= out.begin[r + 1] || r + 1 == out.n_outs) && (out.f32[r] != 0) == wide && maps.valid[r] &&
@@ -384,11 +397,11 @@ __device__ __forceinline__ int slot_range(const OutRanges& out, const OutMaps& m
 
 // The other slots: a warp's 32 rows (from `first` of the CTA's 128), a lane per
 // column.
-__device__ __forceinline__ void store_rows(const OutRanges& out, const uint8_t* slot, bool wide, int c0, int row0,
-                                           int first, int M, int lane) {
+__device__ __forceinline__ void store_rows(const OutRanges& out, const uint8_t* slot, bool wide, int c0, int cols,
+                                           int row0, int first, int M, int lane) {
     const int rows = M - row0 - first < 32 ? M - row0 - first : 32;
     const int elem = wide ? 4 : 2;
-    for (int q = lane; q < (wide ? 64 : 128); q += 32) {
+    for (int q = lane; q < cols; q += 32) {
         const OutColumn o(out, c0 + q);
         if (!o.pitch) continue;
         const int chunk = q * elem >> 4, in = q * elem & 15;
@@ -415,16 +428,18 @@ __device__ __forceinline__ void store_rows(const OutRanges& out, const uint8_t* 
     }
 }
 
+template <int NT>
 __global__ void __launch_bounds__(kPairThreads, 1)
 linear_pair_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUtensorMap map_x,
                    const float* __restrict__ sx, const float* __restrict__ sw, int M, int N, int groups,
                    int tiles_m, int tiles_n, const __grid_constant__ OutRanges out,
                    const __grid_constant__ OutMaps maps) {
-    constexpr int ST = kPairStages;
+    using Lay = PairLayout<NT>;
+    constexpr int ST = Lay::kStages, A = Lay::kAccs, H = Lay::kHalf;
     extern __shared__ uint8_t dyn[];
     uint8_t* smem = align_smem<1024>(dyn);
     __shared__ uint64_t full[ST], empty[ST];
-    __shared__ uint64_t acc_full[4], acc_empty[4];           // 2 * (group & 1) + half
+    __shared__ uint64_t acc_full[2 * A], acc_empty[2 * A];   // 2 * accumulator + half (not split: half 0 for both)
     __shared__ uint64_t slot_full[2], slot_free[2], drained[2];
     __shared__ uint32_t tmem_slot;
     __shared__ int gave_up;
@@ -435,10 +450,10 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_const
 
     if (threadIdx.x == 0) {
         // full: the even CTA's, one arrival (its producer) and both CTAs' bytes;
-        // empty: a commit of either MMA warp; acc_empty: the even CTA's, four
-        // warps of each CTA
-        for (int i = 0; i < ST; ++i) { mbar_init(&full[i], 1); mbar_init(&empty[i], 2); }
-        for (int i = 0; i < 4; ++i) { mbar_init(&acc_full[i], 1); mbar_init(&acc_empty[i], 8); }
+        // empty: a commit of each MMA warp that reads the stage; acc_empty: the
+        // even CTA's, four warps of each CTA for a half
+        for (int i = 0; i < ST; ++i) { mbar_init(&full[i], 1); mbar_init(&empty[i], Lay::kSplit ? 2 : 1); }
+        for (int i = 0; i < 2 * A; ++i) { mbar_init(&acc_full[i], 1); mbar_init(&acc_empty[i], Lay::kSplit ? 8 : 16); }
         for (int i = 0; i < 2; ++i) { mbar_init(&slot_full[i], 4); mbar_init(&slot_free[i], 1); mbar_init(&drained[i], 1); }
         gave_up = 0;
         fence_mbar_init();
@@ -461,16 +476,16 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_const
         for (int t = pair; t < tiles && ok; t += pairs) {
             int tm, tn;
             pair_tile(t, tiles_m, tiles_n, &tm, &tn);
-            const int m0 = tm * 256 + (int)rank * 128, n0 = tn * 256 + (int)rank * 64;
+            const int m0 = tm * 256 + (int)rank * 128, n0 = tn * NT + (int)rank * 64;
             for (int g = 0; g < groups; ++g, ++i) {
                 if (i >= ST && !warp_wait(&empty[s], phase, &gave_up)) { ok = false; break; }
                 if (elect_one()) {
-                    if (rank == 0) mbar_arrive_expect_tx(&full[s], 2 * kPairStageBytes);
+                    if (rank == 0) mbar_arrive_expect_tx(&full[s], 2 * Lay::kStageBytes);
                     const uint32_t bar = cluster_addr(smem_u32(&full[s]), 0);
-                    uint8_t* st = smem + s * kPairStageBytes;
+                    uint8_t* st = smem + s * Lay::kStageBytes;
                     tma_load_2d_pair(st, &map_x, g * kFp8Group, m0, bar);
                     tma_load_2d_pair(st + 16384, &map_w, g * kFp8Group, n0, bar);
-                    tma_load_2d_pair(st + 24576, &map_w, g * kFp8Group, n0 + 128, bar);
+                    if (Lay::kSplit) tma_load_2d_pair(st + 24576, &map_w, g * kFp8Group, n0 + H, bar);
                 }
                 __syncwarp();
                 if (++s == ST) { s = 0; phase ^= 1; }
@@ -484,32 +499,36 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_const
             for (int j = i < ST ? 0 : i - ST; j < i; ++j) mbar_wait(&full[j % ST], (j / ST) & 1);
     } else if (warp == 9 || warp == 10) {
         if (rank == 0) {
+            // 128 columns at a time: of half `mine` in every group, or of every group
+            // whose last bit is `mine`
             constexpr uint32_t idesc = idesc_e4m3_f32(256, 128);
-            const int half = warp - 9;
+            const int mine = warp - 9;
             int i = 0, s = 0, phase = 0;
             bool ok = true;
             for (int t = pair; t < tiles && ok; t += pairs) {
                 for (int g = 0; g < groups; ++g, ++i) {
-                    const int buf = i & 1;
-                    if (!warp_wait(&full[s], phase, &gave_up) ||
-                        (i >= 2 && !warp_wait(&acc_empty[2 * buf + half], ((i >> 1) & 1) ^ 1, &gave_up))) { ok = false; break; }
-                    tc_fence_after_sync();
-                    if (elect_one()) {
-                        const uint32_t a = smem_u32(smem + s * kPairStageBytes);
+                    if (Lay::kSplit || (i & 1) == mine) {
+                        const int buf = i % A, half = Lay::kSplit ? mine : 0;
+                        if (!warp_wait(&full[s], phase, &gave_up) ||
+                            (i >= A && !warp_wait(&acc_empty[2 * buf + half], ((i / A) & 1) ^ 1, &gave_up))) { ok = false; break; }
+                        tc_fence_after_sync();
+                        if (elect_one()) {
+                            const uint32_t a = smem_u32(smem + s * Lay::kStageBytes);
 #pragma unroll
-                        for (int j = 0; j < 4; ++j)      // 32 codes = 16 of the descriptor's 2-byte columns
-                            mma_e4m3_pair(tmem + buf * 256 + half * 128, sw128_desc(a, 128, 0, 16 * j),
-                                          sw128_desc(a + 16384 + half * 8192, 64, 0, 16 * j), idesc, j > 0);
-                        mma_commit_pair(&acc_full[2 * buf + half]);
-                        mma_commit_pair(&empty[s]);
+                            for (int j = 0; j < 4; ++j)      // 32 codes = 16 of the descriptor's 2-byte columns
+                                mma_e4m3_pair(tmem + buf * NT + half * 128, sw128_desc(a, 128, 0, 16 * j),
+                                              sw128_desc(a + 16384 + half * 8192, 64, 0, 16 * j), idesc, j > 0);
+                            mma_commit_pair(&acc_full[2 * buf + half]);
+                            mma_commit_pair(&empty[s]);
+                        }
+                        __syncwarp();
                     }
-                    __syncwarp();
                     if (++s == ST) { s = 0; phase ^= 1; }
                 }
             }
             if (!ok) {
-                if (lane == 0) mma_commit_pair(&drained[half]);
-                mbar_wait(&drained[half], 0);
+                if (lane == 0) mma_commit_pair(&drained[mine]);
+                mbar_wait(&drained[mine], 0);
             }
         }
     } else if (warp == 11) {
@@ -521,19 +540,20 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_const
             const int row0 = tm * 256 + (int)rank * 128;
 #pragma unroll
             for (int half = 0; half < 2; ++half) {
-                const int c0 = tn * 256 + half * 128;
+                const int c0 = tn * NT + half * H;
                 if (c0 >= N || !ok) break;
-                const bool wide = block_is_wide(out, c0, lane);
-                for (int q = 0; q < (wide ? 2 : 1); ++q) {
-                    const int c = c0 + q * 64, r = slot_range(out, maps, wide, c);
+                const bool wide = block_is_wide(out, c0, H, lane);
+                const int cols = wide ? 64 : H;
+                for (int q = 0; q < H; q += cols) {
+                    const int c = c0 + q, r = slot_range(out, maps, wide, c, cols);
                     if (r < 0) continue;                     // warps 0-7 store it
                     if (!warp_wait(&slot_full[half], jobs[half] & 1, &gave_up)) { ok = false; break; }
                     if (elect_one()) {
                         const int off = c - out.begin[r], box = wide ? 32 : 64;
-                        const uint8_t* slot = smem + kPairStaging + half * kPairSlotBytes;
+                        const uint8_t* slot = smem + Lay::kSlots + half * Lay::kSlotBytes;
                         if (row0 < M) {
                             tma_store_2d(&maps.map[r], slot, off, row0);
-                            if (c + box < out.begin[r + 1]) tma_store_2d(&maps.map[r], slot + 16384, off + box, row0);
+                            if (box < cols && c + box < out.begin[r + 1]) tma_store_2d(&maps.map[r], slot + 16384, off + box, row0);
                         }
                         bulk_commit_group();
                         bulk_wait_group_read0();
@@ -547,12 +567,12 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_const
         if (elect_one()) bulk_wait_group0();
     } else {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
-        const int half = warp >> 2;                          // columns half * 128 .. + 127 of the tile
+        const int half = warp >> 2;                          // columns half * H .. + H - 1 of the tile
         const int row = (warp & 3) * 32 + lane;              // row of the CTA's 128
-        const uint32_t at0 = tmem + ((uint32_t)((warp & 3) * 32) << 16) + half * 128;
-        uint8_t* slot = smem + kPairStaging + half * kPairSlotBytes;
-        const uint32_t bar0 = cluster_addr(smem_u32(&acc_empty[half]), 0);
-        const uint32_t bar1 = cluster_addr(smem_u32(&acc_empty[2 + half]), 0);
+        const uint32_t at0 = tmem + ((uint32_t)((warp & 3) * 32) << 16) + half * H;
+        uint8_t* slot = smem + Lay::kSlots + half * Lay::kSlotBytes;
+        const int side = Lay::kSplit ? half : 0;
+        const uint32_t bars = cluster_addr(smem_u32(&acc_empty[side]), 0);
         const bool vec = (groups & 3) == 0 &&
                          ((reinterpret_cast<uint64_t>(sx) | reinterpret_cast<uint64_t>(sw)) & 15) == 0;
         int i = 0, jobs = 0;
@@ -578,19 +598,19 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_const
             pair_tile(t, tiles_m, tiles_n, &tm, &tn);
             m0 = tm * 256 + (int)rank * 128;
             const int m = m0 + row;
-            c0 = tn * 256 + half * 128;
+            c0 = tn * NT + half * H;
             sxp = sx + (int64_t)(m < M ? m : 0) * groups;
-            swp = sw + (int64_t)(c0 < N ? tn * 2 + half : 0) * groups;
+            swp = sw + (int64_t)(c0 < N ? c0 / kFp8Group : 0) * groups;
             fetch(0);
         };
         if (pair < tiles) enter(pair);
         for (int t = pair; t < tiles && ok; t += pairs) {
-            float2 acc[64];
+            float2 acc[H / 2];
 #pragma unroll
-            for (int c = 0; c < 64; ++c) acc[c] = make_float2(0.f, 0.f);
+            for (int c = 0; c < H / 2; ++c) acc[c] = make_float2(0.f, 0.f);
             float4 fs = make_float4(0.f, 0.f, 0.f, 0.f);
             for (int g = 0; g < groups; ++g, ++i) {
-                const int buf = i & 1;
+                const int buf = i % A;
                 if ((g & 3) == 0) {
                     fs = make_float4(nx.x * nw.x, nx.y * nw.y, nx.z * nw.z, nx.w * nw.w);
                     if (g + 4 < groups) fetch(g + 4);
@@ -599,61 +619,70 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_const
                 fs.x = fs.y;
                 fs.y = fs.z;
                 fs.z = fs.w;
-                if (!warp_wait(&acc_full[2 * buf + half], (i >> 1) & 1, &gave_up)) { ok = false; break; }
+                if (!warp_wait(&acc_full[2 * buf + side], (i / A) & 1, &gave_up)) { ok = false; break; }
                 tc_fence_after_sync();
-                const uint32_t at = at0 + buf * 256;
-                // 128 columns as 32 + 16 + 32 + 16 + 32, the next load under way while one is added
+                const uint32_t at = at0 + buf * NT;
+                // the next load under way while one is added
                 float u[32], v[16];
                 tmem_ld32(at, u);
                 tmem_ld_wait_for(u);
                 tmem_ld16(at + 32, v);
                 add_scaled<32>(acc, u, f);
                 tmem_ld_wait_for(v);
-                tmem_ld32(at + 48, u);
-                add_scaled<16>(acc + 16, v, f);
-                tmem_ld_wait_for(u);
-                tmem_ld16(at + 80, v);
-                add_scaled<32>(acc + 24, u, f);
-                tmem_ld_wait_for(v);
-                tmem_ld32(at + 96, u);
-                add_scaled<16>(acc + 40, v, f);
-                tmem_ld_wait_for(u);
-                add_scaled<32>(acc + 48, u, f);
+                if constexpr (H == 128) {            // 32 + 16 + 32 + 16 + 32 columns
+                    tmem_ld32(at + 48, u);
+                    add_scaled<16>(acc + 16, v, f);
+                    tmem_ld_wait_for(u);
+                    tmem_ld16(at + 80, v);
+                    add_scaled<32>(acc + 24, u, f);
+                    tmem_ld_wait_for(v);
+                    tmem_ld32(at + 96, u);
+                    add_scaled<16>(acc + 40, v, f);
+                    tmem_ld_wait_for(u);
+                    add_scaled<32>(acc + 48, u, f);
+                } else {                             // 32 + 16 + 16
+                    float w[16];
+                    tmem_ld16(at + 48, w);
+                    add_scaled<16>(acc + 16, v, f);
+                    tmem_ld_wait_for(w);
+                    add_scaled<16>(acc + 24, w, f);
+                }
                 tc_fence_before_sync();
                 __syncwarp();
-                if (lane == 0) mbar_arrive_cluster(buf ? bar1 : bar0);
+                if (lane == 0) mbar_arrive_cluster(bars + buf * 16);
             }
             const int c_out = c0, m_tile = m0;
             if (t + pairs < tiles) enter(t + pairs);
             if (!ok || c_out >= N) continue;
-            const bool wide = block_is_wide(out, c_out, lane);
+            const bool wide = block_is_wide(out, c_out, H, lane);
+            const int cols = wide ? 64 : H;
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                if (h == 1 && !wide) break;
+            for (int q = 0; q < H; q += 64) {
+                if (q >= 64 && !wide) break;
                 // the slot's last TMA store has read it
                 if (jobs > 0 && !warp_wait(&slot_free[half], (jobs - 1) & 1, &gave_up)) { ok = false; break; }
                 if (wide) {
 #pragma unroll
                     for (int c = 0; c < 16; ++c)
                         *reinterpret_cast<float4*>(slot + slot_chunk(row, c)) =
-                            make_float4(acc[h * 32 + 2 * c].x, acc[h * 32 + 2 * c].y, acc[h * 32 + 2 * c + 1].x,
-                                        acc[h * 32 + 2 * c + 1].y);
+                            make_float4(acc[q / 2 + 2 * c].x, acc[q / 2 + 2 * c].y, acc[q / 2 + 2 * c + 1].x,
+                                        acc[q / 2 + 2 * c + 1].y);
                 } else {
 #pragma unroll
-                    for (int c = 0; c < 16; ++c)
+                    for (int c = 0; c < H / 8; ++c)
                         *reinterpret_cast<uint4*>(slot + slot_chunk(row, c)) =
                             make_uint4(pack_bf16(acc[4 * c].x, acc[4 * c].y), pack_bf16(acc[4 * c + 1].x, acc[4 * c + 1].y),
                                        pack_bf16(acc[4 * c + 2].x, acc[4 * c + 2].y), pack_bf16(acc[4 * c + 3].x, acc[4 * c + 3].y));
                 }
-                const int c = c_out + h * 64;
-                if (slot_range(out, maps, wide, c) >= 0) {
+                const int c = c_out + q;
+                if (slot_range(out, maps, wide, c, cols) >= 0) {
                     fence_proxy_async_smem();
                     __syncwarp();
                     if (lane == 0) mbar_arrive(&slot_full[half]);
                     ++jobs;
                 } else {
                     __syncwarp();
-                    store_rows(out, slot, wide, c, m_tile, (warp & 3) * 32, M, lane);
+                    store_rows(out, slot, wide, c, cols, m_tile, (warp & 3) * 32, M, lane);
                     __syncwarp();
                 }
             }
@@ -770,9 +799,10 @@ cudaError_t launch_few(const gdr_linear_fp8_args& a, EncodeTiledFn enc, cudaStre
                           a.w_scale, (int)a.rows, groups, split, out_ranges(a));
 }
 
+template <int NT>
 cudaError_t launch_pair(const gdr_linear_fp8_args& a, EncodeTiledFn enc, cudaStream_t st) {
     const int groups = fp8_groups(a.k);
-    const int64_t tiles_m = (a.rows + 255) / 256, tiles_n = ((int64_t)a.n + 255) / 256;
+    const int64_t tiles_m = (a.rows + 255) / 256, tiles_n = ((int64_t)a.n + NT - 1) / NT;
     if (tiles_m * tiles_n > (int64_t)INT32_MAX - 1024) return cudaErrorInvalidValue;
     CUtensorMap mw, mx;
     cudaError_t e;
@@ -787,7 +817,7 @@ cudaError_t launch_pair(const gdr_linear_fp8_args& a, EncodeTiledFn enc, cudaStr
         maps.valid[i] = 1;
     }
     const int64_t pairs = tiles_m * tiles_n < kSms / 2 ? tiles_m * tiles_n : kSms / 2;
-    return launch_cluster(linear_pair_kernel, dim3((unsigned)(2 * pairs)), dim3(kPairThreads), kPairDynBytes, 2, st,
+    return launch_cluster(linear_pair_kernel<NT>, dim3((unsigned)(2 * pairs)), dim3(kPairThreads), PairLayout<NT>::kDynBytes, 2, st,
                           mw, mx, a.x_scale, a.w_scale, (int)a.rows, a.n, groups, (int)tiles_m, (int)tiles_n,
                           out_ranges(a), maps);
 }
@@ -800,13 +830,17 @@ cudaError_t launch_linear_fp8(const gdr_linear_fp8_args& a, cudaStream_t st) {
     if (e != cudaSuccess) return e;
     if (a.rows <= 16) return launch_few<16>(a, enc, st);
     if (a.rows <= 32) return launch_few<32>(a, enc, st);
-    // Up to 64 tokens, and more while the tiles of 64 tokens x 128 columns fit the SMs
-    // at once (128 x 4096 x 4096: 11 us against 18 on 16 CTA pairs); beyond that every
-    // weight would be fetched again for each 64 tokens (256 x 16416 x 4096: 51 us
-    // against 22).
+    // Up to 64 tokens, and more while the tiles of 64 tokens x 128 columns fill no more
+    // than half of the SMs (K is then split: 128 x 4096 x 4096 11.3 us, on CTA pairs
+    // 13.3), or all of them where K is short (256 x 3598 x 896: 6.2 against 7.3 us; 256 x
+    // 4096 x 4096: 17.1 against 13.3).  Beyond that each weight would be fetched again
+    // for every 64 tokens (256 x 16416 x 4096: 51 us against 20).
     const int64_t small_tiles = fp8_groups(a.n) * ((a.rows + 63) / 64);
-    if (a.rows <= 64 || small_tiles <= kSms) return launch_few<64>(a, enc, st);
-    return launch_pair(a, enc, st);
+    if (a.rows <= 64 || small_tiles <= kSms / 2 || (small_tiles <= kSms && fp8_groups(a.k) <= 12))
+        return launch_few<64>(a, enc, st);
+    // tiles of 256 x 128 where they fit the CTA pairs at once, else of 256 x 256
+    if ((a.rows + 255) / 256 * fp8_groups(a.n) <= kSms / 2) return launch_pair<128>(a, enc, st);
+    return launch_pair<256>(a, enc, st);
 }
 
 }  // namespace gdr
