@@ -59,7 +59,11 @@ struct OutColumn {
 // second.  The loop is kept this small because it is on every role's critical
 // path: with a look at the timer in it the many-token kernel ran 10 to 30 %
 // slower.
+#ifdef GDR_TEST_WAIT_LIMIT_NS
+constexpr int kWaitTries = 1 << 11;      // the test copy: its MMA warps wait for what nothing sends
+#else
 constexpr int kWaitTries = 1 << 20;
+#endif
 
 template <bool CLUSTER = false>          // whether the phase orders other CTAs' writes
 __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, int* gave_up) {
@@ -129,6 +133,10 @@ linear_few_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_consta
     __shared__ uint64_t full[ST], empty[ST], acc_full[kFewAccs], acc_empty[kFewAccs], drained, parts_bar;
     __shared__ uint32_t tmem_slot;
     __shared__ int gave_up;
+#ifdef GDR_TEST_WAIT_LIMIT_NS
+    __shared__ uint64_t never;
+    if (threadIdx.x == 0) mbar_init(&never, 1);
+#endif
     const int warp = warp_index(), lane = threadIdx.x & 31;
     const int tile = blockIdx.x / split, part = blockIdx.x - tile * split;
     const int n0 = tile * 128, m0 = blockIdx.y * BN;
@@ -182,6 +190,9 @@ linear_few_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_consta
         bool ok = true;
         for (int i = 0, s = 0, phase = 0; i < count; ++i) {
             const int buf = i % kFewAccs;
+#ifdef GDR_TEST_WAIT_LIMIT_NS
+            if (i == 1 && !warp_wait(&never, 0, &gave_up)) { ok = false; break; }
+#endif
             if (!warp_wait(&full[s], phase, &gave_up) ||
                 (i >= kFewAccs && !warp_wait(&acc_empty[buf], ((i / kFewAccs) & 1) ^ 1, &gave_up))) { ok = false; break; }
             tc_fence_after_sync();
@@ -443,6 +454,10 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_const
     __shared__ uint64_t slot_full[2], slot_free[2], drained[2];
     __shared__ uint32_t tmem_slot;
     __shared__ int gave_up;
+#ifdef GDR_TEST_WAIT_LIMIT_NS
+    __shared__ uint64_t never;
+    if (threadIdx.x == 0) mbar_init(&never, 1);
+#endif
     const int warp = warp_index(), lane = threadIdx.x & 31;
     const uint32_t rank = cluster_rank();
     const int pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
@@ -509,6 +524,9 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_const
                 for (int g = 0; g < groups; ++g, ++i) {
                     if (Lay::kSplit || (i & 1) == mine) {
                         const int buf = i % A, half = Lay::kSplit ? mine : 0;
+#ifdef GDR_TEST_WAIT_LIMIT_NS
+                        if (i == 1 && !warp_wait(&never, 0, &gave_up)) { ok = false; break; }
+#endif
                         if (!warp_wait(&full[s], phase, &gave_up) ||
                             (i >= A && !warp_wait(&acc_empty[2 * buf + half], ((i / A) & 1) ^ 1, &gave_up))) { ok = false; break; }
                         tc_fence_after_sync();

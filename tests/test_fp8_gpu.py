@@ -456,3 +456,112 @@ def test_decode_layer_on_fp32_outputs(gdr):
     _check_codes(z, zs, *oracle.gated_norm_fp8(o, gate, L["head_norm"]),
                  SCALE + (4 + 2.4 * float(gate.float().abs().max())) * U)
     _check_linear([out], (z, zs, *w_out), (c,), c)
+
+
+# --- further calls -----------------------------------------------------------------------------
+
+def test_offsets_past_32_bits(gdr):
+    """More than 2^32 elements: the last rows are right, and so are rows in between."""
+    g = _gen(41)
+    rows, width = 131200, 32768                            # 4.3e9 elements
+    x = torch.zeros(rows, width, dtype=bf16, device="cuda")
+    at = torch.tensor([0, 65535, 65536, 131071, 131072, rows - 1], device="cuda")
+    x[at] = torch.randn(at.numel(), width, generator=g, device="cuda").to(bf16)
+    w = 1 + 0.1 * torch.randn(width, generator=g, device="cuda")
+    y, s = gdr.norm_fp8(x, w)
+    torch.cuda.synchronize()
+    rc, rs, _ = oracle.norm_fp8(x[at], w)
+    _check_codes(y[at], s[at], rc, rs, SCALE, "norm")
+    assert not y[1].float().any() and not y[rows - 2].float().any()
+    del y, s
+    gate = torch.zeros(rows, 256, 128, dtype=bf16, device="cuda")
+    y, s = gdr.gated_norm_fp8(x.view(rows, 256, 128), gate, w[:128].contiguous())
+    torch.cuda.synchronize()
+    rc, rs = oracle.gated_norm_fp8(x.view(rows, 256, 128)[at], gate[at], w[:128])
+    _check_codes(y[at], s[at], rc, rs, SCALE + 4 * U, "gated norm")
+    del y, s, gate
+    c, s = gdr.quantize_weight_fp8(x)
+    torch.cuda.synchronize()
+    last = (rows - 1) // 128 * 128
+    rc, rs = oracle.quantize_weight_fp8(x[last:])
+    _check_codes(c[last:], s[last // 128:], rc, rs, 3 * U, "weights")
+    del x, c, s
+    rows, n, k = 66000, 66000, 16                          # 4.36e9 outputs
+    ops = _operands(42, rows, n, k)
+    out = gdr.linear_fp8(*ops)
+    torch.cuda.synchronize()
+    for rs_ in (slice(0, 3), slice(65534, 65540), slice(rows - 3, rows)):
+        sub = (ops[0][rs_], ops[1][rs_], ops[2], ops[3])
+        _check_linear([out[rs_]], sub, [n], k)
+
+
+def test_prepared_calls_follow_stream_and_buffers(gdr):
+    """run() on another stream, and again after its inputs were written anew."""
+    g = _gen(43)
+    x = torch.randn(33, 512, generator=g, device="cuda").to(bf16)
+    w = torch.ones(512, device="cuda")
+    wq = gdr.quantize_weight_fp8(torch.randn(200, 512, generator=g, device="cuda"))
+    norm = gdr.PreparedNormFp8(x, w)
+    lin = gdr.PreparedLinearFp8(*norm.outputs, *wq, out_dtype=f32)
+    side = torch.cuda.Stream()
+    for i in range(3):
+        x.copy_(torch.randn(33, 512, generator=g, device="cuda"))
+        side.wait_stream(torch.cuda.current_stream())
+        norm.run(stream=side)
+        assert lin.run(stream=side) is lin.outputs
+        torch.cuda.current_stream().wait_stream(side)
+        ref = gdr.linear_fp8(*gdr.norm_fp8(x, w), *wq, out_dtype=f32)
+        assert torch.equal(lin.outputs, ref)
+
+
+def test_two_graphs_of_the_same_calls_at_once(gdr):
+    """Nothing is shared between calls: two captured graphs replayed on two streams."""
+    cases = [_operands(51, 40, 600, 2048), _operands(52, 900, 600, 1024)]
+    refs = [gdr.linear_fp8(*o, out_dtype=f32).clone() for o in cases]
+    torch.cuda.synchronize()
+    graphs = []
+    for o in cases:
+        plan = gdr.PreparedLinearFp8(*o, out_dtype=f32)
+        plan.run()
+        torch.cuda.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            for _ in range(20):
+                plan.run()
+        graphs.append((graph, plan, torch.cuda.Stream()))
+    for graph, plan, st in graphs:
+        plan.outputs.zero_()
+    torch.cuda.synchronize()
+    for _ in range(5):
+        for graph, plan, st in graphs:
+            with torch.cuda.stream(st):
+                graph.replay()
+    torch.cuda.synchronize()
+    for (graph, plan, st), r in zip(graphs, refs):
+        assert torch.equal(plan.outputs, r)
+    gdr.linear_fp8_status()
+
+
+def test_products_beside_a_prefill_on_another_stream(gdr):
+    """The product's kernels and the prefill's hold tensor memory on the same SMs."""
+    import workloads as wl
+    w = wl.shrink(wl.VARLEN, n_heads=4, d_k=64, d_v=64, lengths=(700, 300), init_std=0.1, snap_interval=0)
+    d = {k: (v.cuda() if torch.is_tensor(v) else v) for k, v in wl.make_prefill_inputs(w).items()}
+    pre = lambda: gdr.prefill(d["q"], d["k"], d["v"], d["beta"], d["log_a"], d["cu_seqlens"],
+                              init_state=d["init_state"], cu_seqlens_host=d["cu_seqlens"].cpu())[0]
+    cases = [_operands(61, 30, 2000, 2048), _operands(62, 300, 2000, 1024), _operands(63, 2000, 2000, 512)]
+    refs = [gdr.linear_fp8(*o) for o in cases]
+    o_ref = pre()
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(4)]
+    outs, os_ = [], []
+    for _ in range(8):
+        with torch.cuda.stream(streams[3]):
+            os_.append(pre())
+        for o, r, st in zip(cases, refs, streams):
+            with torch.cuda.stream(st):
+                outs.append((gdr.linear_fp8(*o), r))
+    torch.cuda.synchronize()
+    assert all(torch.equal(y, r) for y, r in outs)
+    assert all(torch.equal(o, o_ref) for o in os_)
+    gdr.linear_fp8_status()
