@@ -6,8 +6,9 @@ Tolerances, derived from the arithmetic (u = 2^-24, half an fp32 step):
   thread, 5 warp shuffles and 16 warps' sums (85 u, halved by the square root),
   one rounding of h (u), rsqrtf (2 ulp = 4 u), the mean's division, two
   products and the division by 448 (4 u): under 54 u = 3.2e-6.  SCALE = 4e-6.
-* gated_norm_fp8: the sums are shorter, the sigmoid adds the error of __expf
-  (2 + 1.173 |g| ulp of 2 u), two roundings and a 2-ulp division:
+* gated_norm_fp8: the sums are shorter (16 products, 3 shuffles); the sigmoid adds
+  the rounding of g log2 e (2 |g| u in the power, with the constant's), the 2-ulp
+  power and reciprocal and three roundings, which the shorter sums make room for:
   SCALE + (4 + 2.4 |g|) u.
 * a code: y / scale carries the error of y, of the scale's reciprocal (2 u) and
   one rounding more, together under twice the scale's tolerance, and is then
