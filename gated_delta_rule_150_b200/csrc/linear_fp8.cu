@@ -189,12 +189,12 @@ linear_few_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_consta
         constexpr uint32_t idesc = idesc_e4m3_f32(128, BN);
         bool ok = true;
         for (int i = 0, s = 0, phase = 0; i < count; ++i) {
-            const int buf = i % kFewAccs;
+            const int buf = (unsigned)i % kFewAccs;
 #ifdef GDR_TEST_WAIT_LIMIT_NS
             if (i == 1 && !warp_wait(&never, 0, &gave_up)) { ok = false; break; }
 #endif
             if (!warp_wait(&full[s], phase, &gave_up) ||
-                (i >= kFewAccs && !warp_wait(&acc_empty[buf], ((i / kFewAccs) & 1) ^ 1, &gave_up))) { ok = false; break; }
+                (i >= kFewAccs && !warp_wait(&acc_empty[buf], (((unsigned)i / kFewAccs) & 1) ^ 1, &gave_up))) { ok = false; break; }
             tc_fence_after_sync();
             if (elect_one()) {
                 const uint32_t a = smem_u32(smem + s * Lay::kStageBytes);
@@ -235,14 +235,14 @@ linear_few_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_consta
         fetch(g0);
         bool ok = true;
         for (int i = 0; i < count; ++i) {
-            const int buf = i % kFewAccs;
+            const int buf = (unsigned)i % kFewAccs;
             float* f = factors + (i & 1) * BN;
 #pragma unroll
             for (int p = 0; p < kPer; ++p)
                 if (BN >= 32 || lane < BN) f[p * 32 + lane] = next[p];
             if (i + 1 < count) fetch(g0 + i + 1);
             __syncwarp();
-            if (!warp_wait(&acc_full[buf], (i / kFewAccs) & 1, &gave_up)) { ok = false; break; }
+            if (!warp_wait(&acc_full[buf], ((unsigned)i / kFewAccs) & 1, &gave_up)) { ok = false; break; }
             tc_fence_after_sync();
             const uint32_t at = tmem + ((uint32_t)(warp * 32) << 16) + buf * BN;
             float d[BN / kLoad][kLoad];
@@ -523,12 +523,12 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_const
             for (int t = pair; t < tiles && ok; t += pairs) {
                 for (int g = 0; g < groups; ++g, ++i) {
                     if (Lay::kSplit || (i & 1) == mine) {
-                        const int buf = i % A, half = Lay::kSplit ? mine : 0;
+                        const int buf = (unsigned)i % A, half = Lay::kSplit ? mine : 0;
 #ifdef GDR_TEST_WAIT_LIMIT_NS
                         if (i == 1 && !warp_wait(&never, 0, &gave_up)) { ok = false; break; }
 #endif
                         if (!warp_wait(&full[s], phase, &gave_up) ||
-                            (i >= A && !warp_wait(&acc_empty[2 * buf + half], ((i / A) & 1) ^ 1, &gave_up))) { ok = false; break; }
+                            (i >= A && !warp_wait(&acc_empty[2 * buf + half], (((unsigned)i / A) & 1) ^ 1, &gave_up))) { ok = false; break; }
                         tc_fence_after_sync();
                         if (elect_one()) {
                             const uint32_t a = smem_u32(smem + s * Lay::kStageBytes);
@@ -628,7 +628,7 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_const
             for (int c = 0; c < H / 2; ++c) acc[c] = make_float2(0.f, 0.f);
             float4 fs = make_float4(0.f, 0.f, 0.f, 0.f);
             for (int g = 0; g < groups; ++g, ++i) {
-                const int buf = i % A;
+                const int buf = (unsigned)i % A;
                 if ((g & 3) == 0) {
                     fs = make_float4(nx.x * nw.x, nx.y * nw.y, nx.z * nw.z, nx.w * nw.w);
                     if (g + 4 < groups) fetch(g + 4);
@@ -637,7 +637,7 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_const
                 fs.x = fs.y;
                 fs.y = fs.z;
                 fs.z = fs.w;
-                if (!warp_wait(&acc_full[2 * buf + side], (i / A) & 1, &gave_up)) { ok = false; break; }
+                if (!warp_wait(&acc_full[2 * buf + side], ((unsigned)i / A) & 1, &gave_up)) { ok = false; break; }
                 tc_fence_after_sync();
                 const uint32_t at = at0 + buf * NT;
                 // the next load under way while one is added
