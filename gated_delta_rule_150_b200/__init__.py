@@ -768,6 +768,12 @@ FP8_GROUP = 128
 NORM_MAX_WIDTH = 32768
 
 
+def _io_dtype(t, name) -> int:
+    if t.dtype not in (torch.bfloat16, torch.float32):
+        raise TypeError(f"{name} must be bfloat16 or float32, got {t.dtype}")
+    return _dtype_code(t)
+
+
 def _groups(width: int) -> int:
     return -(-width // FP8_GROUP)
 
@@ -859,7 +865,7 @@ class PreparedNormFp8(_Prepared):
                  residual_out=None):
         _expect_dim(x, 2, "x")
         rows, width = x.shape
-        dtype = _dtype_code(x)
+        dtype = _io_dtype(x, "x")
         if width % 16 or not 16 <= width <= NORM_MAX_WIDTH:
             raise ValueError(f"width must be a multiple of 16 up to {NORM_MAX_WIDTH}, got {width}")
         _expect(norm_weight, (width,), torch.float32, "norm_weight")
@@ -928,7 +934,7 @@ class PreparedGatedNormFp8(_Prepared):
         _check_eps(norm_eps)
         a = GatedNormFp8Args()
         a.rows, a.n_heads, a.d_v = rows, H, d
-        a.o_dtype, a.gate_dtype = _dtype_code(o), _dtype_code(gate_raw)
+        a.o_dtype, a.gate_dtype = _io_dtype(o, "o"), _io_dtype(gate_raw, "gate_raw")
         _need_one_device(o, gate_raw, norm_weight, out, out_scale)
         given = not (out is None and out_scale is None)
         if out is None:
@@ -962,7 +968,7 @@ def quantize_weight_fp8(w, *, out=None, out_scale=None):
     [N, K] and one fp32 scale per 128 x 128 block [ceil(N / 128), ceil(K / 128)]."""
     _expect_dim(w, 2, "w")
     n, k = w.shape
-    dtype = _dtype_code(w)
+    dtype = _io_dtype(w, "w")
     if k % 16 or k < 16:
         raise ValueError(f"K must be a positive multiple of 16, got {k}")
     _expect(out, (n, k), torch.float8_e4m3fn, "out")

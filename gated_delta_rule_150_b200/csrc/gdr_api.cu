@@ -113,7 +113,7 @@ const char* gdr_status_string(gdr_status s) {
     return "GDR_ERR_UNKNOWN";
 }
 
-int gdr_version(void) { return 100; }
+int gdr_version(void) { return 200; }
 
 size_t gdr_prefill_workspace_size(int n_seqs, int n_heads, int d_k, int d_v,
                                   int64_t total_tokens, int scalar_decay) {

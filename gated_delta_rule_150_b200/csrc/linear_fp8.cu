@@ -571,7 +571,7 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_const
                     if (elect_one()) {
                         const int off = c - out.begin[r], box = wide ? 32 : 64;
                         const uint8_t* slot = smem + Lay::kSlots + half * Lay::kSlotBytes;
-                        if (row0 < M) {
+                        if (row0 < M && c < out.begin[r + 1]) {      // a box starts inside its tensor
                             tma_store_2d(&maps.map[r], slot, off, row0);
                             if (box < cols && c + box < out.begin[r + 1]) tma_store_2d(&maps.map[r], slot + 16384, off + box, row0);
                         }

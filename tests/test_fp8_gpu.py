@@ -246,6 +246,21 @@ def test_linear_columns_and_depths(gdr, rows, n, k):
     _check_linear([y], ops, [n], k)
 
 
+@pytest.mark.parametrize("rows", [700, 2100, 20000])
+@pytest.mark.parametrize("n", [8, 132, 200, 264, 520, 776])
+@pytest.mark.parametrize("dt", [bf16, f32])
+def test_linear_last_tile_partly_empty(gdr, rows, n, dt):
+    """Rows that TMA can store, and a last tile with less than half of its columns."""
+    ops = _operands(rows + n, rows, n, 144)
+    buf = torch.full((rows * n + 2 * 128,), 77.0, dtype=dt, device="cuda")
+    out = buf[128:128 + rows * n].view(rows, n)
+    gdr.linear_fp8(*ops, out_dtype=dt, out=out)
+    torch.cuda.synchronize()
+    at = torch.cat([torch.arange(0, 40), torch.arange(rows - 40, rows)]).cuda()
+    _check_linear([out[at]], (ops[0][at], ops[1][at], *ops[2:]), [n], 144)
+    assert (buf[:128] == 77).all() and (buf[-128:] == 77).all()
+
+
 @pytest.mark.parametrize("rows", [1, 20, 200, 1030])
 @pytest.mark.parametrize("cols,kinds", [((896, 896, 896, 896, 14), "bbbff"), ((130, 3, 1), "bfb"), ((1, 255), "fb"),
                                         ((64,) * 8, "bfbfbfbf"), ((256, 257, 127), "fbf")])
