@@ -552,21 +552,35 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_const
             }
         }
     } else if (warp == 11) {
-        int jobs[2] = {0, 0};
+        // A slot is given back once its store has read it; while a store is under way
+        // the other slot's is started (`pending`: the slot still to be given back).
+        // The warp blocks on a slot only when it owes none, so no adder can wait for it
+        // in a circle.
+        int jobs[2] = {0, 0}, pending = -1;
         bool ok = true;
+        const auto give_back = [&] {
+            if (pending >= 0 && elect_one()) {
+                bulk_wait_group_read0();
+                mbar_arrive(&slot_free[pending]);
+            }
+            __syncwarp();
+            pending = -1;
+        };
         for (int t = pair; t < tiles && ok; t += pairs) {
             int tm, tn;
             pair_tile(t, tiles_m, tiles_n, &tm, &tn);
             const int row0 = tm * 256 + (int)rank * 128;
+            for (int q = 0; q < H && ok; q += 64) {
 #pragma unroll
-            for (int half = 0; half < 2; ++half) {
-                const int c0 = tn * NT + half * H;
-                if (c0 >= N || !ok) break;
-                const bool wide = block_is_wide(out, c0, H, lane);
-                const int cols = wide ? 64 : H;
-                for (int q = 0; q < H; q += cols) {
-                    const int c = c0 + q, r = slot_range(out, maps, wide, c, cols);
-                    if (r < 0) continue;                     // warps 0-7 store it
+                for (int half = 0; half < 2; ++half) {
+                    const int c0 = tn * NT + half * H, c = c0 + q;
+                    if (c0 >= N || !ok) break;
+                    const bool wide = block_is_wide(out, c0, H, lane);
+                    const int cols = wide ? 64 : H;
+                    const int r = q < H && q % cols == 0 ? slot_range(out, maps, wide, c, cols) : -1;
+                    if (r < 0) continue;                     // no such round, or warps 0-7 store it
+                    if (pending >= 0 && !__all_sync(0xffffffffu, mbar_test_wait(smem_u32(&slot_full[half]), jobs[half] & 1)))
+                        give_back();
                     if (!warp_wait(&slot_full[half], jobs[half] & 1, &gave_up)) { ok = false; break; }
                     if (elect_one()) {
                         const int off = c - out.begin[r], box = wide ? 32 : 64;
@@ -576,14 +590,18 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_const
                             if (box < cols && c + box < out.begin[r + 1]) tma_store_2d(&maps.map[r], slot + 16384, off + box, row0);
                         }
                         bulk_commit_group();
-                        bulk_wait_group_read0();
-                        mbar_arrive(&slot_free[half]);
+                        if (pending >= 0) {
+                            bulk_wait_group_read<1>();
+                            mbar_arrive(&slot_free[pending]);
+                        }
                     }
                     __syncwarp();
+                    pending = half;
                     ++jobs[half];
                 }
             }
         }
+        give_back();
         if (elect_one()) bulk_wait_group0();
     } else {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
