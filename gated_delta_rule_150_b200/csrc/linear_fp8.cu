@@ -374,14 +374,6 @@ __device__ __forceinline__ void pair_tile(int t, int tiles_m, int tiles_n, int* 
     *tm = first + (r - *tn * rows);
 }
 
-// Whether any of the `cols` columns from c0 on goes to an fp32 tensor: their outputs
-// then pass through shared memory as fp32 (64 columns at a time), otherwise as bf16.
-__device__ __forceinline__ bool block_is_wide(const OutRanges& out, int c0, int cols, int lane) {
-    bool wide = false;
-    if (lane < out.n_outs) wide = out.f32[lane] && out.begin[lane] < c0 + cols && out.begin[lane + 1] > c0;
-    return __any_sync(0xffffffffu, wide);
-}
-
 // Where the 16-byte chunk c (0 .. 15) of a row's 256 bytes lies in an output slot:
 // two boxes of 128 rows x 128 bytes, 128-byte swizzle (no bank conflicts, and the
 // layout a TMA store reads).
@@ -396,17 +388,35 @@ struct OutMaps {
     int valid[GDR_LINEAR_MAX_OUTS];
 };
 
-// The range that a slot of outputs goes to by TMA (`cols` columns from c0, all in one
-// range with a map, at a 16-byte boundary of its rows), or -1.  What lies past the
-// last range's columns is dropped by the store.
-__device__ __forceinline__ int slot_range(const OutRanges& out, const OutMaps& maps, bool wide, int c0, int cols) {
-    const int elem = wide ? 4 : 2;
-    int r = 0;
-    while (r + 1 < out.n_outs && c0 >= out.begin[r + 1]) ++r;
-    const bool ok = (c0 + cols <= out.begin[r + 1] || r + 1 == out.n_outs) && (out.f32[r] != 0) == wide && maps.valid[r] &&
-                    ((c0 - out.begin[r]) * elem & 15) == 0;
-    return ok ? r : -1;
-}
+// A warp's view of the output ranges, a lane per range: what a block of columns is
+// then takes a vote instead of a walk through the parameters (which took the store
+// warp 900 cycles a block, longer than a short K's sums).
+struct RangeLane {
+    int begin, end;
+    bool f32, mapped, last;
+    __device__ __forceinline__ RangeLane(const OutRanges& out, const OutMaps& maps, int lane)
+        : begin(0), end(0), f32(false), mapped(false), last(lane == out.n_outs - 1) {
+        if (lane < out.n_outs) {
+            begin = out.begin[lane];
+            end = out.begin[lane + 1];
+            f32 = out.f32[lane] != 0;
+            mapped = maps.valid[lane] != 0;
+        }
+    }
+    // Whether any of the `cols` columns from c0 on goes to an fp32 tensor: their outputs
+    // then pass through shared memory as fp32 (64 columns at a time), otherwise as bf16.
+    __device__ __forceinline__ bool wide(int c0, int cols) const {
+        return __any_sync(0xffffffffu, f32 && begin < c0 + cols && end > c0);
+    }
+    // The range that a slot of outputs goes to by TMA (`cols` columns from c0, all in
+    // one range with a map, at a 16-byte boundary of its rows), or -1.  What lies past
+    // the last range's columns is dropped by the store.
+    __device__ __forceinline__ int slot_range(bool is_wide, int c0, int cols) const {
+        const bool mine = begin <= c0 && c0 < end && (c0 + cols <= end || last) && f32 == is_wide && mapped &&
+                          ((c0 - begin) * (is_wide ? 4 : 2) & 15) == 0;
+        return __ffs(__ballot_sync(0xffffffffu, mine)) - 1;
+    }
+};
 
 // The other slots: a warp's 32 rows (from `first` of the CTA's 128), a lane per
 // column.
@@ -566,26 +576,27 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_const
             __syncwarp();
             pending = -1;
         };
+        const RangeLane ranges(out, maps, lane);
         for (int t = pair; t < tiles && ok; t += pairs) {
             int tm, tn;
             pair_tile(t, tiles_m, tiles_n, &tm, &tn);
             const int row0 = tm * 256 + (int)rank * 128;
+            const bool wides[2] = {ranges.wide(tn * NT, H), ranges.wide(tn * NT + H, H)};
             for (int q = 0; q < H && ok; q += 64) {
 #pragma unroll
                 for (int half = 0; half < 2; ++half) {
-                    const int c0 = tn * NT + half * H, c = c0 + q;
-                    if (c0 >= N || !ok) break;
-                    const bool wide = block_is_wide(out, c0, H, lane);
-                    const int cols = wide ? 64 : H;
-                    const int r = q < H && q % cols == 0 ? slot_range(out, maps, wide, c, cols) : -1;
-                    if (r < 0) continue;                     // no such round, or warps 0-7 store it
+                    const bool wide = wides[half];
+                    if (!ok || (q > 0 && !wide)) continue;
+                    const int cols = wide ? 64 : H, c = tn * NT + half * H + q;
+                    const int r = ranges.slot_range(wide, c, cols);
+                    if (r < 0) continue;                     // past the columns, or warps 0-7 store it
                     if (pending >= 0 && !__all_sync(0xffffffffu, mbar_test_wait(smem_u32(&slot_full[half]), jobs[half] & 1)))
                         give_back();
                     if (!warp_wait(&slot_full[half], jobs[half] & 1, &gave_up)) { ok = false; break; }
                     if (elect_one()) {
                         const int off = c - out.begin[r], box = wide ? 32 : 64;
                         const uint8_t* slot = smem + Lay::kSlots + half * Lay::kSlotBytes;
-                        if (row0 < M && c < out.begin[r + 1]) {      // a box starts inside its tensor
+                        if (row0 < M) {                      // a box starts inside its tensor
                             tma_store_2d(&maps.map[r], slot, off, row0);
                             if (box < cols && c + box < out.begin[r + 1]) tma_store_2d(&maps.map[r], slot + 16384, off + box, row0);
                         }
@@ -631,9 +642,9 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_const
                                  __ldg(swp + min(g + 3, last)));
             }
         };
-        const auto enter = [&](int t) {
-            int tm, tn;
-            pair_tile(t, tiles_m, tiles_n, &tm, &tn);
+        const RangeLane ranges(out, maps, lane);
+        int tm = 0, tn = 0;                                  // the tile that enter() goes to
+        const auto enter = [&] {
             m0 = tm * 256 + (int)rank * 128;
             const int m = m0 + row;
             c0 = tn * NT + half * H;
@@ -641,8 +652,14 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_const
             swp = sw + (int64_t)(c0 < N ? c0 / kFp8Group : 0) * groups;
             fetch(0);
         };
-        if (pair < tiles) enter(pair);
+        if (pair < tiles) {
+            pair_tile(pair, tiles_m, tiles_n, &tm, &tn);
+            enter();
+        }
         for (int t = pair; t < tiles && ok; t += pairs) {
+            const int c_out = c0, m_tile = m0;
+            const bool wide = ranges.wide(c_out, H);
+            if (t + pairs < tiles) pair_tile(t + pairs, tiles_m, tiles_n, &tm, &tn);
             float2 acc[H / 2];
 #pragma unroll
             for (int c = 0; c < H / 2; ++c) acc[c] = make_float2(0.f, 0.f);
@@ -689,10 +706,8 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_const
                 __syncwarp();
                 if (lane == 0) mbar_arrive_cluster(bars + buf * 16);
             }
-            const int c_out = c0, m_tile = m0;
-            if (t + pairs < tiles) enter(t + pairs);
+            if (t + pairs < tiles) enter();
             if (!ok || c_out >= N) continue;
-            const bool wide = block_is_wide(out, c_out, H, lane);
             const int cols = wide ? 64 : H;
 #pragma unroll
             for (int q = 0; q < H; q += 64) {
@@ -713,7 +728,7 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_const
                                        pack_bf16(acc[4 * c + 2].x, acc[4 * c + 2].y), pack_bf16(acc[4 * c + 3].x, acc[4 * c + 3].y));
                 }
                 const int c = c_out + q;
-                if (slot_range(out, maps, wide, c, cols) >= 0) {
+                if (ranges.slot_range(wide, c, cols) >= 0) {
                     fence_proxy_async_smem();
                     __syncwarp();
                     if (lane == 0) mbar_arrive(&slot_full[half]);
