@@ -235,6 +235,7 @@ linear_few_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_consta
             }
         };
         fetch(g0);
+        const OutColumn o(out, n0 + threadIdx.x);    // while the first loads are on their way
         bool ok = true;
         for (int i = 0; i < count; ++i) {
             const int buf = (unsigned)i % kFewAccs;
@@ -269,7 +270,6 @@ linear_few_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_consta
         }
         tc_fence_before_sync();
         asm volatile("bar.arrive 1, 160;" ::: "memory");
-        const OutColumn o(out, n0 + threadIdx.x);
         if (split == 1) {
             if (o.pitch)
 #pragma unroll
