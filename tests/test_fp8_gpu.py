@@ -581,3 +581,28 @@ def test_products_beside_a_prefill_on_another_stream(gdr):
     assert all(torch.equal(y, r) for y, r in outs)
     assert all(torch.equal(o, o_ref) for o in os_)
     gdr.linear_fp8_status()
+
+
+@pytest.mark.parametrize("cols,kinds", [((3598,), "b"), ((1001,), "b"), ((1001,), "f"), ((2050,), "f"), ((896, 14, 1030), "bfb"),
+                                        ((129, 70, 57, 1000), "bfbf"), ((3, 14, 777, 5, 300, 1, 131, 260), "bbfbbfbf")])
+@pytest.mark.parametrize("rows", [515, 4099])
+def test_linear_rows_at_any_alignment(gdr, rows, cols, kinds):
+    """Products for many tokens whose output rows start at any element, in the middle
+    of larger buffers.  Each output is its sum rounded once, so it is equal to one
+    wide fp32 product (or that, rounded), and what lies around it stays."""
+    n, k = sum(cols), 272
+    wide = -(-n // 8) * 8 + 8                          # the reference's rows are aligned
+    x, xs, w, ws = _operands(rows + n, rows, wide, k)
+    ref = gdr.linear_fp8(x, xs, w, ws, out_dtype=f32)
+    at = torch.cat([torch.arange(0, 3), torch.arange(rows - 3, rows)]).cuda()
+    _check_linear([ref[at]], (x[at], xs[at], w, ws), [wide], k)
+    dts = [bf16 if c == "b" else f32 for c in kinds]
+    ws_n = ws[:-(-n // 128)].contiguous()
+    for lead in (128, 131, 134, 137):
+        bufs = [torch.full((rows * c + lead + 128,), 77.0, dtype=t, device="cuda") for c, t in zip(cols, dts)]
+        outs = [b[lead:lead + rows * c].view(rows, c) for b, c in zip(bufs, cols)]
+        gdr.linear_fp8(x, xs, w[:n].contiguous(), ws_n, splits=cols, out_dtype=dts, out=outs)
+        for o, b, r, t in zip(outs, bufs, ref[:, :n].split(cols, 1), dts):
+            assert torch.equal(o, r.to(t))
+            assert (b[:lead] == 77).all() and (b[-128:] == 77).all()
+    gdr.linear_fp8_status()
