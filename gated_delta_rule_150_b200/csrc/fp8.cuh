@@ -100,4 +100,25 @@ __device__ __forceinline__ uint2 fp8_codes(const float* y, float inv_scale) {
     return make_uint2(h[0] | (h[1] << 16), h[2] | (h[3] << 16));
 }
 
+// The same with the quotient y / scale itself: where y is given and not rounded
+// before, as a weight is, quotients on the border between two codes are common, and
+// they have to come out exact to go to the even code.  The first quotient's remainder
+// y - q scale, exact in one fused operation, gives the second (P. Markstein, IBM J.
+// Res. Dev. 34, 1990); a quotient that fp32 holds comes out as it is.  16416 x 4096
+// bf16: 31.0 us, as without the correction; 63 with a division per value.
+// An infinite scale's inverse is 0, and 0 times y is left.
+__device__ __forceinline__ uint2 fp8_codes_divided(const float* y, float scale, float inv_scale) {
+    float q[8];
+    const float2 inv = make_float2(inv_scale, inv_scale), neg = make_float2(-scale, -scale);
+#pragma unroll
+    for (int i = 0; i < 8; i += 2) {
+        const float2 v = make_float2(y[i], y[i + 1]);
+        float2 t = __fmul2_rn(v, inv);
+        if (inv_scale > 0.f) t = __ffma2_rn(__ffma2_rn(t, neg, v), inv, t);
+        q[i] = t.x;
+        q[i + 1] = t.y;
+    }
+    return fp8_codes(q, 1.f);
+}
+
 }  // namespace gdr

@@ -176,6 +176,30 @@ def test_quantize_weight(gdr, n, k, dt):
     _check_codes(c, s, rc, rs, 3 * U, "weights")
 
 
+@pytest.mark.parametrize("dt", [bf16, f32])
+@pytest.mark.parametrize("n,k", [(127, 400), (1000, 896)])
+def test_quantize_weight_ties_go_to_the_even_code(gdr, n, k, dt):
+    """Multiples of 1/4 under a largest value of 448 times a power of two: every
+    quotient is exact, and many lie halfway between two codes."""
+    g = _gen(n + k)
+    w = torch.randint(-1791, 1792, (n, k), generator=g, device="cuda").float() / 4
+    if dt == bf16:                             # 8 significant bits, one more than a tie needs
+        w = w.to(bf16).float()
+    w[::128, ::128] = 448.0
+    power = torch.exp2(torch.randint(-9, 3, (-(-n // 128), -(-k // 128)), generator=g, device="cuda").float())
+    w = w * power.repeat_interleave(128, 0)[:n].repeat_interleave(128, 1)[:, :k]
+    c, s = gdr.quantize_weight_fp8(w.to(dt))
+    torch.cuda.synchronize()
+    assert torch.equal(s, power)
+    rc, _ = oracle.quantize_weight_fp8(w)
+    assert np.array_equal(_np(c), oracle.e4m3(rc))
+    # any scale: the code of the quotient as fp32 rounds it
+    w = (0.03 * torch.randn(n, k, generator=g, device="cuda")).to(dt)
+    c, s = gdr.quantize_weight_fp8(w)
+    q = w.float() / s.repeat_interleave(128, 0)[:n].repeat_interleave(128, 1)[:, :k]
+    assert np.array_equal(_np(c), oracle.e4m3(q))
+
+
 def test_quantize_weight_special_blocks(gdr):
     w = torch.randn(256, 256, generator=_gen(11), device="cuda")
     w[:128, :128] = 0
