@@ -120,8 +120,16 @@ __device__ __forceinline__ float rcp_approx(float x) {
     return y;
 }
 
+// CTAs per SM that the registers have to leave room for: eight, at which all loads are
+// issued before the first is used (16384 x 7 x 64 with fp32 gates: 10.5 us, 12.9 when
+// the compiler chooses; 8192 x 32 x 128 with fp32 o: 39.6 against 41.9; 2048 x 14 x 64
+// bf16: 3.8 against 4.3), and ten for bf16 heads of 128, where more warps hide more
+// (16384 x 32 x 128: 60.3 us in a graph, 63.6 with eight).
 template <typename TO, typename TG, int D>
-__global__ void __launch_bounds__(kGatedThreads)
+constexpr int gated_ctas() { return sizeof(TO) + sizeof(TG) == 4 && D == 128 ? 10 : 8; }
+
+template <typename TO, typename TG, int D>
+__global__ void __launch_bounds__(kGatedThreads, gated_ctas<TO, TG, D>())
 gated_norm_fp8_kernel(int64_t tasks, int groups, int n16, const TO* __restrict__ o,
                       const TG* __restrict__ gate, const float* __restrict__ weight, float eps,
                       uint8_t* __restrict__ y, float* __restrict__ y_scale) {
