@@ -15,23 +15,23 @@ namespace {
 
 // ---------------------------------------------------------------------------
 // y = h / sqrt(mean h^2 + eps) * w with h = x + residual.
-// A row belongs to a warp (ROWS = 4 rows per CTA, up to 64 octets) or to a whole
-// CTA (ROWS = 1), each thread with up to IT octets of it, kept in registers as
-// fp32 between the sum of squares and the codes.  Octet j of a row belongs to the
+// A row belongs to half a warp (ROWS = 8 rows per CTA, up to 16 octets), to a warp
+// (ROWS = 4, up to 64) or to a whole CTA (ROWS = 1), each thread with up to IT octets
+// of it, kept in registers as fp32 between the sum of squares and the codes.  Octet j of a row belongs to the
 // row's group j / 16, so an aligned half warp holds exactly one group.
 // ---------------------------------------------------------------------------
 template <typename T, bool RES, int ROWS, int IT>
-__global__ void __launch_bounds__(ROWS > 1 ? 32 * ROWS : IT > 2 ? 512 : 1024)
+__global__ void __launch_bounds__(ROWS > 1 ? 128 : IT > 2 ? 512 : 1024)
 norm_fp8_kernel(int rows, int width, const T* x, const T* residual, const float* __restrict__ weight,
                 float eps, T* residual_out, uint8_t* __restrict__ y, float* __restrict__ y_scale) {
     __shared__ float part[32];
     pdl_wait();
     pdl_launch_dependents();
-    const int TPR = ROWS > 1 ? 32 : blockDim.x;
-    const int t = ROWS > 1 ? threadIdx.x & 31 : threadIdx.x;
-    const int row = ROWS > 1 ? blockIdx.x * ROWS + (threadIdx.x >> 5) : blockIdx.x;
-    if (ROWS > 1 && row >= rows) return;           // whole warps
-    const int n8 = width >> 3;
+    const int TPR = ROWS > 1 ? 128 / ROWS : blockDim.x;
+    const int t = ROWS > 1 ? threadIdx.x % (128 / ROWS) : threadIdx.x;
+    const int row = ROWS > 1 ? blockIdx.x * ROWS + threadIdx.x / (128 / ROWS) : blockIdx.x;
+    if (ROWS == 4 && row >= rows) return;          // whole warps
+    const int n8 = ROWS > 4 && row >= rows ? 0 : width >> 3;
     const int64_t base = (int64_t)row * width;
     Octet<T> a[IT], b[IT];
 #pragma unroll
@@ -66,7 +66,7 @@ norm_fp8_kernel(int rows, int width, const T* x, const T* residual, const float*
         }
     }
 #pragma unroll
-    for (int s = 16; s > 0; s >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, s);
+    for (int s = ROWS > 1 ? 64 / ROWS : 16; s > 0; s >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, s);
     if (ROWS == 1) {
         if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = ss;
         __syncthreads();
@@ -252,13 +252,18 @@ cudaError_t launch_norm_shape(const gdr_norm_fp8_args& a, int threads, cudaStrea
 
 // Two octets a thread: 8192 rows of 896 take 10.4 us with 64 threads a row, 11.5
 // with one warp of four octets, 11.3 with 128 of one; 65536 rows of 2048 take 139
-// us (1.03 of the copy rate) with 128 threads, 145 with a warp, 157 with 256.  With too few rows to fill
-// the SMs one octet a thread (a single row of 896: 2.2 against 2.4 us).
+// us (1.03 of the copy rate) with 128 threads, 145 with a warp, 157 with 256.  Several
+// rows to a CTA of 256 threads are slower (16384 rows of 896: 22.1 against 20.5 us): they
+// load and wait together.  With too few rows to fill the SMs one octet a thread (a single
+// row of 896: 2.2 against 2.4 us).  Rows of one group would leave half of a warp idle:
+// two to a warp (65536 rows of 64: 10.1 against 20.2 us; 100000 of 128: 16.8 against
+// 30.4).
 template <typename T, bool RES>
 cudaError_t launch_norm_typed(const gdr_norm_fp8_args& a, cudaStream_t st) {
     const int n8 = a.width / 8;
     const auto warps = [n8](int it) { return 32 * ((n8 + 32 * it - 1) / (32 * it)); };
     if (a.rows <= 2 * 148 && n8 <= 1024) return launch_norm_shape<T, RES, 1, 1>(a, warps(1), st);
+    if (n8 <= 16) return launch_norm_shape<T, RES, 8, 1>(a, 128, st);
     if (n8 <= 64) return launch_norm_shape<T, RES, 4, 2>(a, 128, st);
     if (n8 <= 2048) return launch_norm_shape<T, RES, 1, 2>(a, warps(2), st);
     return launch_norm_shape<T, RES, 1, 8>(a, warps(8), st);

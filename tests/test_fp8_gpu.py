@@ -630,3 +630,11 @@ def test_linear_rows_at_any_alignment(gdr, rows, cols, kinds):
             assert torch.equal(o, r.to(t))
             assert (b[:lead] == 77).all() and (b[-128:] == 77).all()
     gdr.linear_fp8_status()
+
+
+@pytest.mark.parametrize("rows", [297, 300, 303, 1001, 40001])
+@pytest.mark.parametrize("width", [16, 64, 112, 128, 144, 240, 256, 272])
+@pytest.mark.parametrize("dt,residual", [(bf16, True), (f32, False), (f32, True)])
+def test_norm_many_narrow_rows(gdr, rows, width, dt, residual):
+    """More than one row to a warp, and a last warp that is not full."""
+    _check_norm(gdr, rows, width, dt, residual, seed=2)
