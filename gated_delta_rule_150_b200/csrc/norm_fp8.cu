@@ -103,8 +103,8 @@ norm_fp8_kernel(int rows, int width, const T* x, const T* residual, const float*
 // Eight lanes own one group of 128 channels of a token (one head at D 128, two at
 // D 64), 16 channels each: half the shuffles and divisions per channel of eight
 // channels a lane.  Bound by HBM with the issue slots close behind (16384 tokens of
-// 32 x 128, bf16: 66 us or 0.78 of the copy rate; 82 us with eight channels a lane,
-// 71 before the arithmetic went two channels to an instruction).
+// 32 x 128, bf16: 65 us in a stream of calls or 0.79 of the copy rate; 82 us with eight
+// channels a lane, 71 before the arithmetic went two channels to an instruction).
 // ---------------------------------------------------------------------------
 constexpr int kGatedThreads = 128;
 
