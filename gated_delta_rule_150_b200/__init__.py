@@ -766,6 +766,7 @@ def snapshot_offload(dev_snapshots, host_snapshots, copy_stream, event, compute_
 # ---------------------------------------------------------------------------
 FP8_GROUP = 128
 NORM_MAX_WIDTH = 32768
+FP8_MAX_SIZE = 2 ** 31 - 1024      # rows, widths, N and K (the argument blocks hold 32 bits of them)
 
 
 def _io_dtype(t, name) -> int:
@@ -776,6 +777,12 @@ def _io_dtype(t, name) -> int:
 
 def _groups(width: int) -> int:
     return -(-width // FP8_GROUP)
+
+
+def _need_sizes(**sizes):
+    for name, n in sizes.items():
+        if n > FP8_MAX_SIZE:
+            raise ValueError(f"{name} must be at most {FP8_MAX_SIZE}, got {n}")
 
 
 def _need_one_device(*ts):
@@ -866,6 +873,7 @@ class PreparedNormFp8(_Prepared):
         _expect_dim(x, 2, "x")
         rows, width = x.shape
         dtype = _io_dtype(x, "x")
+        _need_sizes(rows=rows)
         if width % 16 or not 16 <= width <= NORM_MAX_WIDTH:
             raise ValueError(f"width must be a multiple of 16 up to {NORM_MAX_WIDTH}, got {width}")
         _expect(norm_weight, (width,), torch.float32, "norm_weight")
@@ -927,6 +935,7 @@ class PreparedGatedNormFp8(_Prepared):
             raise ValueError(f"d_v must be 64 or 128, got {d}")
         if H < 1:
             raise ValueError("o needs at least one head")
+        _need_sizes(rows=rows, **{"H * d_v": H * d})
         _expect(gate_raw, (rows, H, d), None, "gate_raw")
         _expect(norm_weight, (d,), torch.float32, "norm_weight")
         _expect(out, (rows, H * d), torch.float8_e4m3fn, "out")
@@ -969,6 +978,7 @@ def quantize_weight_fp8(w, *, out=None, out_scale=None):
     _expect_dim(w, 2, "w")
     n, k = w.shape
     dtype = _io_dtype(w, "w")
+    _need_sizes(N=n, K=k)
     if k % 16 or k < 16:
         raise ValueError(f"K must be a positive multiple of 16, got {k}")
     _expect(out, (n, k), torch.float8_e4m3fn, "out")
@@ -998,6 +1008,7 @@ class PreparedLinearFp8(_Prepared):
         _expect_dim(w, 2, "w")
         rows, k = x.shape
         n = w.shape[0]
+        _need_sizes(rows=rows, N=n, K=k)
         if k % 16 or k < 16:
             raise ValueError(f"K must be a positive multiple of 16, got {k}")
         if n < 1:
