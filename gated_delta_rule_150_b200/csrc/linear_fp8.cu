@@ -211,7 +211,7 @@ linear_few_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_consta
             if (++s == ST) { s = 0; phase ^= 1; }
         }
         if (!ok) {
-            if (lane == 0) mma_commit(&drained);
+            if (elect_one()) mma_commit(&drained);       // a commit counts its own thread's MMAs only
             mbar_wait(&drained, 0);
         }
         __syncwarp();
@@ -557,7 +557,7 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_const
                 }
             }
             if (!ok) {
-                if (lane == 0) mma_commit_pair(&drained[mine]);
+                if (elect_one()) mma_commit_pair(&drained[mine]);    // a commit counts its own thread's MMAs only
                 mbar_wait(&drained[mine], 0);
             }
         }

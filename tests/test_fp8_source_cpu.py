@@ -1,0 +1,42 @@
+"""Rules of the 8-bit product's kernels that no run on a healthy GPU shows, held on
+the source text (linear_fp8.cu): where they break, a kernel that gives up a wait
+would release memory that is still written."""
+import os
+import re
+
+import pytest
+
+from gated_delta_rule_150_b200 import build as gdr_build
+
+
+def _source():
+    with open(os.path.join(gdr_build.CSRC, "linear_fp8.cu")) as f:
+        return re.sub(r"//[^\n]*", "", f.read())
+
+
+def _enclosing_ifs(src, at):
+    """Conditions of the `if`s around position `at`: of each open block, and of the
+    statement itself."""
+    conds, depth = [], 0
+    start = max(src.rfind(c, 0, at) for c in ";{}")
+    conds += re.findall(r"if \((.*)\)\s*$", src[start + 1:at].strip() + "\n", re.M)
+    for i in range(at - 1, -1, -1):
+        if src[i] == "}":
+            depth += 1
+        elif src[i] == "{":
+            if depth:
+                depth -= 1
+            else:
+                head = src[max(src.rfind(c, 0, i) for c in ";{}") + 1:i]
+                conds += re.findall(r"if \((.*)\)\s*$", head.strip() + "\n", re.M | re.S)
+    return conds
+
+
+@pytest.mark.parametrize("call", ["mma_e4m3(", "mma_e4m3_pair(", "mma_commit(", "mma_commit_pair("])
+def test_mmas_and_their_commits_are_issued_by_the_elected_lane(call):
+    """A commit follows the MMAs of the thread that issues it, and no other's."""
+    src = _source()
+    places = [m.start() for m in re.finditer(r"(?<![\w])" + re.escape(call), src)]
+    assert places
+    for at in places:
+        assert any("elect_one()" in c for c in _enclosing_ifs(src, at)), src[at - 80:at + 40]
