@@ -19,8 +19,8 @@ namespace {
 
 constexpr int kSms = 148;
 
-// Set by a kernel that gave up a bounded wait; read and cleared by
-// gdr_linear_fp8_status.
+// Set by a kernel that gave up a bounded wait (1), or a wait for what it had in
+// flight then (2); read and cleared by gdr_linear_fp8_status.
 __device__ uint32_t g_linear_error;
 
 // The output's column ranges: columns begin[i] .. begin[i + 1] - 1 go to the
@@ -74,6 +74,21 @@ __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, int* g
     atomicOr(&g_linear_error, 1u);
     return false;
 }
+
+// After a give-up: wait, again with a limit, for what this CTA has in flight.
+__device__ __forceinline__ void drain_wait(uint64_t* bar, uint32_t parity) {
+    if (!mbar_wait(bar, parity)) atomicOr(&g_linear_error, 2u);
+}
+
+// The test copy: one role (0: MMAs, 1: loads, 2: loads of odd CTAs, 3: sums) waits, at
+// its second group, for a barrier that nothing arrives on.
+#ifdef GDR_TEST_WAIT_LIMIT_NS
+__device__ int g_linear_test_role;
+#define GDR_TEST_STALLS(role, i) \
+    ((i) == 1 && *(volatile int*)&g_linear_test_role == (role) && !warp_wait(&never, 0, &gave_up))
+#else
+#define GDR_TEST_STALLS(role, i) false
+#endif
 
 // The warp's number from one lane, so that the compiler knows it to be the same in
 // all of them and keeps what depends on it in uniform registers (the many-token
@@ -170,11 +185,12 @@ linear_few_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_consta
     pdl_wait();
     pdl_launch_dependents();
 
+    bool parts_due = false;              // this warp gave up its wait for the parts
     if (warp == 4) {
         int i = 0;
-        bool ok = true;
         for (int s = 0, phase = 1; i < count; ++i) {
-            if (i >= ST && !warp_wait(&empty[s], phase, &gave_up)) { ok = false; break; }
+            if (GDR_TEST_STALLS(1, i) || (part % 2 == 1 && GDR_TEST_STALLS(2, i)) ||
+                (i >= ST && !warp_wait(&empty[s], phase, &gave_up))) break;
             if (elect_one()) {
                 uint8_t* st = smem + s * Lay::kStageBytes;
                 mbar_arrive_expect_tx(&full[s], Lay::kStageBytes);
@@ -184,19 +200,14 @@ linear_few_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_consta
             __syncwarp();
             if (++s == ST) { s = 0; phase ^= 1; }
         }
-        // gave up: no copy may still be in flight when the CTA ends
-        if (!ok)
-            for (int j = i < ST ? 0 : i - ST; j < i; ++j) mbar_wait(&full[j % ST], (j / ST) & 1);
+        // no copy may still be in flight when the CTA ends, whichever role gave up
+        for (int j = i < ST ? 0 : i - ST; j < i; ++j) drain_wait(&full[j % ST], (j / ST) & 1);
     } else if (warp == 5) {
         constexpr uint32_t idesc = idesc_e4m3_f32(128, BN);
-        bool ok = true;
         for (int i = 0, s = 0, phase = 0; i < count; ++i) {
             const int buf = (unsigned)i % kFewAccs;
-#ifdef GDR_TEST_WAIT_LIMIT_NS
-            if (i == 1 && !warp_wait(&never, 0, &gave_up)) { ok = false; break; }
-#endif
-            if (!warp_wait(&full[s], phase, &gave_up) ||
-                (i >= kFewAccs && !warp_wait(&acc_empty[buf], (((unsigned)i / kFewAccs) & 1) ^ 1, &gave_up))) { ok = false; break; }
+            if (GDR_TEST_STALLS(0, i) || !warp_wait(&full[s], phase, &gave_up) ||
+                (i >= kFewAccs && !warp_wait(&acc_empty[buf], (((unsigned)i / kFewAccs) & 1) ^ 1, &gave_up))) break;
             tc_fence_after_sync();
             if (elect_one()) {
                 const uint32_t a = smem_u32(smem + s * Lay::kStageBytes);
@@ -210,13 +221,14 @@ linear_few_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_consta
             __syncwarp();
             if (++s == ST) { s = 0; phase ^= 1; }
         }
-        if (!ok) {
-            if (elect_one()) mma_commit(&drained);       // a commit counts its own thread's MMAs only
-            mbar_wait(&drained, 0);
-        }
         __syncwarp();
         asm volatile("bar.sync 1, 160;" ::: "memory");       // warps 0-3 have read their sums
         tc_fence_after_sync();
+        if (*(volatile int*)&gave_up) {                      // this warp, or one of them: MMAs may be under way
+            if (elect_one()) mma_commit(&drained);           // a commit counts its own thread's MMAs only
+            drain_wait(&drained, 0);
+            __syncwarp();
+        }
         tmem_dealloc(tmem, Lay::kTmemCols);
     } else {
         float acc[BN];
@@ -236,7 +248,6 @@ linear_few_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_consta
         };
         fetch(g0);
         const OutColumn o(out, n0 + threadIdx.x);    // while the first loads are on their way
-        bool ok = true;
         for (int i = 0; i < count; ++i) {
             const int buf = (unsigned)i % kFewAccs;
             float* f = factors + (i & 1) * BN;
@@ -245,7 +256,7 @@ linear_few_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_consta
                 if (BN >= 32 || lane < BN) f[p * 32 + lane] = next[p];
             if (i + 1 < count) fetch(g0 + i + 1);
             __syncwarp();
-            if (!warp_wait(&acc_full[buf], ((unsigned)i / kFewAccs) & 1, &gave_up)) { ok = false; break; }
+            if (GDR_TEST_STALLS(3, i) || !warp_wait(&acc_full[buf], ((unsigned)i / kFewAccs) & 1, &gave_up)) break;
             tc_fence_after_sync();
             const uint32_t at = tmem + ((uint32_t)(warp * 32) << 16) + buf * BN;
             float d[BN / kLoad][kLoad];
@@ -287,7 +298,8 @@ linear_few_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_consta
                               cluster_addr(bar, owner));
                 if (++owner == split) { owner = 0; ++slot; }
             }
-            if (owned > 0 && warp_wait<true>(&parts_bar, 0, &gave_up)) {
+            parts_due = owned > 0 && !warp_wait<true>(&parts_bar, 0, &gave_up);
+            if (owned > 0 && !parts_due) {
                 const float4* parts = reinterpret_cast<const float4*>(smem + Lay::kParts) + threadIdx.x;
                 for (int j = 0; j < owned; ++j) {
                     float4 v = parts[(j * split) * 128];
@@ -308,10 +320,11 @@ linear_few_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_consta
     }
     if (split > 1) {
         // no CTA may end while a part is on its way to it; owners have waited for
-        // theirs, so nothing else has to be ordered here
+        // theirs, so nothing else has to be ordered here.  Every CTA sends all its
+        // parts, whatever it gave up, so after this they have at least been sent.
         __syncwarp();
         asm volatile("barrier.cluster.arrive.relaxed.aligned;\n\tbarrier.cluster.wait.aligned;" ::: "memory");
-        if (*(volatile int*)&gave_up) __nanosleep(100000);
+        if (parts_due) drain_wait(&parts_bar, 0);
     }
 }
 
@@ -919,3 +932,17 @@ extern "C" gdr_status gdr_linear_fp8_status(void* stream) {
     }
     return GDR_ERR_TIMEOUT;
 }
+
+#ifdef GDR_TEST_WAIT_LIMIT_NS
+// The test copy's role that waits for nothing, and the error word as it is (cleared).
+extern "C" int gdr_linear_fp8_test_role(int role) {
+    return (int)cudaMemcpyToSymbol(gdr::g_linear_test_role, &role, sizeof(role));
+}
+
+extern "C" int gdr_linear_fp8_test_word(void) {
+    uint32_t word = 0, zero = 0;
+    if (cudaMemcpyFromSymbol(&word, gdr::g_linear_error, sizeof(word)) != cudaSuccess ||
+        cudaMemcpyToSymbol(gdr::g_linear_error, &zero, sizeof(zero)) != cudaSuccess) return -1;
+    return (int)word;
+}
+#endif
