@@ -58,7 +58,7 @@ struct OutColumn {
 // suspends the warp for up to about a microsecond, so the limit is about a
 // second.  The loop is kept this small because it is on every role's critical
 // path: with a look at the timer in it the many-token kernel ran 10 to 30 %
-// slower.
+// slower, with one more store after the limit 2 to 4 %.
 #ifdef GDR_TEST_WAIT_LIMIT_NS
 constexpr int kWaitTries = 1 << 11;      // the test copy: its MMA warps wait for what nothing sends
 #else
@@ -66,11 +66,10 @@ constexpr int kWaitTries = 1 << 20;
 #endif
 
 template <bool CLUSTER = false>          // whether the phase orders other CTAs' writes
-__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, int* gave_up) {
+__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity) {
     const uint32_t a = smem_u32(bar);
     for (int i = 0; i < kWaitTries; ++i)
         if (__all_sync(0xffffffffu, CLUSTER ? mbar_try_wait_cluster(a, parity) : mbar_try_wait(a, parity))) return true;
-    *gave_up = 1;
     atomicOr(&g_linear_error, 1u);
     return false;
 }
@@ -80,12 +79,13 @@ __device__ __forceinline__ void drain_wait(uint64_t* bar, uint32_t parity) {
     if (!mbar_wait(bar, parity)) atomicOr(&g_linear_error, 2u);
 }
 
-// The test copy: one role (0: MMAs, 1: loads, 2: loads of odd CTAs, 3: sums) waits, at
-// its second group, for a barrier that nothing arrives on.
+// The test copy: one role (0: MMAs, 1: loads, 2: loads of odd CTAs, 3: sums; of CTA
+// pairs also 4: stores, 5: loads of even CTAs) waits, at its second group, for a
+// barrier that nothing arrives on.
 #ifdef GDR_TEST_WAIT_LIMIT_NS
 __device__ int g_linear_test_role;
 #define GDR_TEST_STALLS(role, i) \
-    ((i) == 1 && *(volatile int*)&g_linear_test_role == (role) && !warp_wait(&never, 0, &gave_up))
+    ((i) == 1 && *(volatile int*)&g_linear_test_role == (role) && !wait(&never, 0))
 #else
 #define GDR_TEST_STALLS(role, i) false
 #endif
@@ -186,11 +186,16 @@ linear_few_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_consta
     pdl_launch_dependents();
 
     bool parts_due = false;              // this warp gave up its wait for the parts
+    const auto wait = [&](uint64_t* bar, uint32_t parity) {
+        if (warp_wait(bar, parity)) return true;
+        gave_up = 1;
+        return false;
+    };
     if (warp == 4) {
         int i = 0;
         for (int s = 0, phase = 1; i < count; ++i) {
             if (GDR_TEST_STALLS(1, i) || (part % 2 == 1 && GDR_TEST_STALLS(2, i)) ||
-                (i >= ST && !warp_wait(&empty[s], phase, &gave_up))) break;
+                (i >= ST && !wait(&empty[s], phase))) break;
             if (elect_one()) {
                 uint8_t* st = smem + s * Lay::kStageBytes;
                 mbar_arrive_expect_tx(&full[s], Lay::kStageBytes);
@@ -206,8 +211,8 @@ linear_few_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_consta
         constexpr uint32_t idesc = idesc_e4m3_f32(128, BN);
         for (int i = 0, s = 0, phase = 0; i < count; ++i) {
             const int buf = (unsigned)i % kFewAccs;
-            if (GDR_TEST_STALLS(0, i) || !warp_wait(&full[s], phase, &gave_up) ||
-                (i >= kFewAccs && !warp_wait(&acc_empty[buf], (((unsigned)i / kFewAccs) & 1) ^ 1, &gave_up))) break;
+            if (GDR_TEST_STALLS(0, i) || !wait(&full[s], phase) ||
+                (i >= kFewAccs && !wait(&acc_empty[buf], (((unsigned)i / kFewAccs) & 1) ^ 1))) break;
             tc_fence_after_sync();
             if (elect_one()) {
                 const uint32_t a = smem_u32(smem + s * Lay::kStageBytes);
@@ -256,7 +261,7 @@ linear_few_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_consta
                 if (BN >= 32 || lane < BN) f[p * 32 + lane] = next[p];
             if (i + 1 < count) fetch(g0 + i + 1);
             __syncwarp();
-            if (GDR_TEST_STALLS(3, i) || !warp_wait(&acc_full[buf], ((unsigned)i / kFewAccs) & 1, &gave_up)) break;
+            if (GDR_TEST_STALLS(3, i) || !wait(&acc_full[buf], ((unsigned)i / kFewAccs) & 1)) break;
             tc_fence_after_sync();
             const uint32_t at = tmem + ((uint32_t)(warp * 32) << 16) + buf * BN;
             float d[BN / kLoad][kLoad];
@@ -298,7 +303,7 @@ linear_few_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_consta
                               cluster_addr(bar, owner));
                 if (++owner == split) { owner = 0; ++slot; }
             }
-            parts_due = owned > 0 && !warp_wait<true>(&parts_bar, 0, &gave_up);
+            parts_due = owned > 0 && !warp_wait<true>(&parts_bar, 0);
             if (owned > 0 && !parts_due) {
                 const float4* parts = reinterpret_cast<const float4*>(smem + Lay::kParts) + threadIdx.x;
                 for (int j = 0; j < owned; ++j) {
@@ -464,6 +469,32 @@ __device__ __forceinline__ void store_rows(const OutRanges& out, const uint8_t* 
     }
 }
 
+// After its loading warp gave up, on the even CTA, whose `full` barriers count both
+// CTAs' loads: wait for all that were issued (`mine` groups here, *peers_plus_1 - 1 by
+// the odd CTA, once its loading warp ended).  The CTAs may have stopped at different
+// groups, at most STAGES apart: a stage is loaded anew only after both CTAs' last loads
+// of it were used, so all but the last STAGES loads have landed.  Bytes that this CTA
+// announced for loads its peer never made are taken off the barrier, and loads that
+// only the peer made are announced.  (If this warp did not give up, it saw every stage
+// used: both CTAs' loads have landed.)
+template <int STAGES>
+__device__ void drain_pair_loads(uint64_t* full, uint32_t stage_bytes, int mine, const volatile int* peers_plus_1) {
+    const uint64_t t0 = global_timer_ns();
+    while (*peers_plus_1 == 0)
+        if (global_timer_ns() - t0 > kWaitLimitNs) {
+            atomicOr(&g_linear_error, 2u);
+            return;
+        }
+    const int peers = *peers_plus_1 - 1;
+    const int last = mine > peers ? mine : peers;
+    for (int j = last < STAGES ? 0 : last - STAGES; j < last; ++j) {
+        uint64_t* bar = &full[j % STAGES];
+        if (j >= peers) mbar_complete_tx(bar, stage_bytes);
+        if (j >= mine) mbar_arrive_expect_tx(bar, stage_bytes);
+        drain_wait(bar, (j / STAGES) & 1);
+    }
+}
+
 template <int NT>
 __global__ void __launch_bounds__(kPairThreads, 1)
 linear_pair_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUtensorMap map_x,
@@ -478,7 +509,7 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_const
     __shared__ uint64_t acc_full[2 * A], acc_empty[2 * A];   // 2 * accumulator + half (not split: half 0 for both)
     __shared__ uint64_t slot_full[2], slot_free[2], drained[2];
     __shared__ uint32_t tmem_slot;
-    __shared__ int gave_up;
+    __shared__ int peers_plus_1;                             // even CTA: groups that the odd one loaded, + 1
 #ifdef GDR_TEST_WAIT_LIMIT_NS
     __shared__ uint64_t never;
     if (threadIdx.x == 0) mbar_init(&never, 1);
@@ -495,7 +526,7 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_const
         for (int i = 0; i < ST; ++i) { mbar_init(&full[i], 1); mbar_init(&empty[i], Lay::kSplit ? 2 : 1); }
         for (int i = 0; i < 2 * A; ++i) { mbar_init(&acc_full[i], 1); mbar_init(&acc_empty[i], Lay::kSplit ? 8 : 16); }
         for (int i = 0; i < 2; ++i) { mbar_init(&slot_full[i], 4); mbar_init(&slot_free[i], 1); mbar_init(&drained[i], 1); }
-        gave_up = 0;
+        peers_plus_1 = 0;
         fence_mbar_init();
     }
     __syncwarp();
@@ -510,6 +541,7 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_const
 
     // registers: 256 threads x 216 + 128 x 72 = the launch's 384 x 168
     if (warp >= 8) asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
+    const auto wait = [](uint64_t* bar, uint32_t parity) { return warp_wait(bar, parity); };
     if (warp == 8) {
         int i = 0, s = 0, phase = 1;
         bool ok = true;
@@ -518,7 +550,8 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_const
             pair_tile(t, tiles_m, tiles_n, &tm, &tn);
             const int m0 = tm * 256 + (int)rank * 128, n0 = tn * NT + (int)rank * 64;
             for (int g = 0; g < groups; ++g, ++i) {
-                if (i >= ST && !warp_wait(&empty[s], phase, &gave_up)) { ok = false; break; }
+                if (GDR_TEST_STALLS(1, i) || GDR_TEST_STALLS(rank == 1 ? 2 : 5, i) ||
+                    (i >= ST && !wait(&empty[s], phase))) { ok = false; break; }
                 if (elect_one()) {
                     if (rank == 0) mbar_arrive_expect_tx(&full[s], 2 * Lay::kStageBytes);
                     const uint32_t bar = cluster_addr(smem_u32(&full[s]), 0);
@@ -531,12 +564,13 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_const
                 if (++s == ST) { s = 0; phase ^= 1; }
             }
         }
-        // the last stages' releases must have landed before this CTA's shared
-        // memory goes; after a give-up, so must its copies (they are counted
-        // on the even CTA's barriers)
-        for (int j = i < ST ? 0 : i - ST; j < i && ok; ++j) ok = warp_wait(&empty[j % ST], (j / ST) & 1, &gave_up);
-        if (!ok && rank == 0)
-            for (int j = i < ST ? 0 : i - ST; j < i; ++j) mbar_wait(&full[j % ST], (j / ST) & 1);
+        // the last stages' releases must have landed before this CTA's shared memory goes
+        for (int j = i < ST ? 0 : i - ST; j < i && ok; ++j) ok = wait(&empty[j % ST], (j / ST) & 1);
+        if (lane == 0) {
+            if (rank == 1) st_cluster(cluster_addr(smem_u32(&peers_plus_1), 0), i + 1);
+            else if (!ok) drain_pair_loads<ST>(full, Lay::kStageBytes, i, &peers_plus_1);
+        }
+        __syncwarp();
     } else if (warp == 9 || warp == 10) {
         if (rank == 0) {
             // 128 columns at a time: of half `mine` in every group, or of every group
@@ -549,11 +583,8 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_const
                 for (int g = 0; g < groups; ++g, ++i) {
                     if (Lay::kSplit || (i & 1) == mine) {
                         const int buf = (unsigned)i % A, half = Lay::kSplit ? mine : 0;
-#ifdef GDR_TEST_WAIT_LIMIT_NS
-                        if (i == 1 && !warp_wait(&never, 0, &gave_up)) { ok = false; break; }
-#endif
-                        if (!warp_wait(&full[s], phase, &gave_up) ||
-                            (i >= A && !warp_wait(&acc_empty[2 * buf + half], (((unsigned)i / A) & 1) ^ 1, &gave_up))) { ok = false; break; }
+                        if (GDR_TEST_STALLS(0, i) || !wait(&full[s], phase) ||
+                            (i >= A && !wait(&acc_empty[2 * buf + half], (((unsigned)i / A) & 1) ^ 1))) { ok = false; break; }
                         tc_fence_after_sync();
                         if (elect_one()) {
                             const uint32_t a = smem_u32(smem + s * Lay::kStageBytes);
@@ -569,10 +600,10 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_const
                     if (++s == ST) { s = 0; phase ^= 1; }
                 }
             }
-            if (!ok) {
-                if (elect_one()) mma_commit_pair(&drained[mine]);    // a commit counts its own thread's MMAs only
-                mbar_wait(&drained[mine], 0);
-            }
+            // no MMA may still be under way when tensor memory is released, whichever role
+            // gave up; a commit counts its own thread's MMAs only
+            if (elect_one()) mma_commit_pair(&drained[mine]);
+            drain_wait(&drained[mine], 0);
         }
     } else if (warp == 11) {
         // A slot is given back once its store has read it; while a store is under way
@@ -605,7 +636,7 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_const
                     if (r < 0) continue;                     // past the columns, or warps 0-7 store it
                     if (pending >= 0 && !__all_sync(0xffffffffu, mbar_test_wait(smem_u32(&slot_full[half]), jobs[half] & 1)))
                         give_back();
-                    if (!warp_wait(&slot_full[half], jobs[half] & 1, &gave_up)) { ok = false; break; }
+                    if (GDR_TEST_STALLS(4, jobs[0] + jobs[1]) || !wait(&slot_full[half], jobs[half] & 1)) { ok = false; break; }
                     if (elect_one()) {
                         const int off = c - out.begin[r], box = wide ? 32 : 64;
                         const uint8_t* slot = smem + Lay::kSlots + half * Lay::kSlotBytes;
@@ -687,7 +718,7 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_const
                 fs.x = fs.y;
                 fs.y = fs.z;
                 fs.z = fs.w;
-                if (!warp_wait(&acc_full[2 * buf + side], ((unsigned)i / A) & 1, &gave_up)) { ok = false; break; }
+                if (GDR_TEST_STALLS(3, i) || !wait(&acc_full[2 * buf + side], ((unsigned)i / A) & 1)) { ok = false; break; }
                 tc_fence_after_sync();
                 const uint32_t at = at0 + buf * NT;
                 // the next load under way while one is added
@@ -726,7 +757,7 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_const
             for (int q = 0; q < H; q += 64) {
                 if (q >= 64 && !wide) break;
                 // the slot's last TMA store has read it
-                if (jobs > 0 && !warp_wait(&slot_free[half], (jobs - 1) & 1, &gave_up)) { ok = false; break; }
+                if (jobs > 0 && !wait(&slot_free[half], (jobs - 1) & 1)) { ok = false; break; }
                 if (wide) {
 #pragma unroll
                     for (int c = 0; c < 16; ++c)

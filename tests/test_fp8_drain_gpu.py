@@ -12,7 +12,7 @@ import pytest
 import torch
 
 pytestmark = pytest.mark.gpu
-MMAS, LOADS, ODD_LOADS, SUMS = range(4)
+MMAS, LOADS, ODD_LOADS, SUMS, STORES, EVEN_LOADS = range(6)
 TIMEOUT, OK = 5, 0
 
 
@@ -64,4 +64,13 @@ PARTS = [(3, 256, 2048), (30, 512, 4096), (50, 512, 4096), (130, 1024, 4096)]
 @pytest.mark.parametrize("rows,n,k,role", [(*c, r) for c in WHOLE for r in (MMAS, LOADS, SUMS)] +
                          [(*c, r) for c in PARTS for r in (MMAS, LOADS, ODD_LOADS, SUMS)])
 def test_few_tokens(libs, rows, n, k, role):
+    _stop(libs, role, rows, n, k)
+
+
+# CTA pairs on 256 x 128 and on 256 x 256 tiles, one tile or several a pair.  Where one
+# CTA of a pair stops loading, the other is up to all stages ahead of it.
+@pytest.mark.parametrize("role", [MMAS, LOADS, ODD_LOADS, SUMS, STORES, EVEN_LOADS])
+@pytest.mark.parametrize("rows,n,k", [(300, 4096, 256), (300, 4096, 2048), (1024, 8192, 256), (1024, 8192, 1024),
+                                      (9000, 2048, 128), (2100, 1000, 4096)])
+def test_cta_pairs(libs, rows, n, k, role):
     _stop(libs, role, rows, n, k)
