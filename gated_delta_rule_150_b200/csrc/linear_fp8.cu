@@ -173,18 +173,14 @@ linear_few_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_consta
         if (split > 1) mbar_arrive_expect_tx(&parts_bar, (uint32_t)(owned * split) * Lay::kPartBytes);
     }
     // Every CTA's barrier must be ready for its peers' parts.  TMEM is held only
-    // where no other CTA is waited for (before this and after the sums), so that
-    // clusters which share SMs cannot wait for each other's columns.
+    // where no other CTA or kernel is waited for (from the previous kernel's end to the
+    // sums), so that clusters which share SMs cannot wait for each other's columns, nor
+    // a previous kernel, which may let this one start before it allocates, for this
+    // one's.  The loads start beside the allocation (some 320 cycles).
     __syncwarp();
     if (split > 1) cluster_sync();
-    if (warp == 5) tmem_alloc(&tmem_slot, Lay::kTmemCols);
-    tc_fence_before_sync();
-    __syncthreads();
-    tc_fence_after_sync();
-    const uint32_t tmem = tmem_slot;
+    else __syncthreads();
     pdl_wait();
-    pdl_launch_dependents();
-
     bool parts_due = false;              // this warp gave up its wait for the parts
     const auto wait = [&](uint64_t* bar, uint32_t parity) {
         if (warp_wait(bar, parity)) return true;
@@ -209,6 +205,12 @@ linear_few_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_consta
         for (int j = i < ST ? 0 : i - ST; j < i; ++j) drain_wait(&full[j % ST], (j / ST) & 1);
     } else if (warp == 5) {
         constexpr uint32_t idesc = idesc_e4m3_f32(128, BN);
+        tmem_alloc(&tmem_slot, Lay::kTmemCols);
+        pdl_launch_dependents();                             // not before: the next kernel may want TMEM too
+        __syncwarp();
+        tc_fence_before_sync();
+        asm volatile("bar.arrive 2, 160;" ::: "memory");     // for warps 0-3
+        const uint32_t tmem = *(volatile uint32_t*)&tmem_slot;
         for (int i = 0, s = 0, phase = 0; i < count; ++i) {
             const int buf = (unsigned)i % kFewAccs;
             if (GDR_TEST_STALLS(0, i) || !wait(&full[s], phase) ||
@@ -253,6 +255,9 @@ linear_few_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_consta
         };
         fetch(g0);
         const OutColumn o(out, n0 + threadIdx.x);    // while the first loads are on their way
+        asm volatile("bar.sync 2, 160;" ::: "memory");       // warp 5 has allocated
+        tc_fence_after_sync();
+        const uint32_t tmem = *(volatile uint32_t*)&tmem_slot;
         for (int i = 0; i < count; ++i) {
             const int buf = (unsigned)i % kFewAccs;
             float* f = factors + (i & 1) * BN;
@@ -507,7 +512,7 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_const
     uint8_t* smem = align_smem<1024>(dyn);
     __shared__ uint64_t full[ST], empty[ST];
     __shared__ uint64_t acc_full[2 * A], acc_empty[2 * A];   // 2 * accumulator + half (not split: half 0 for both)
-    __shared__ uint64_t slot_full[2], slot_free[2], drained[2];
+    __shared__ uint64_t slot_full[2], slot_free[2], drained[2], peer_tmem;
     __shared__ uint32_t tmem_slot;
     __shared__ int peers_plus_1;                             // even CTA: groups that the odd one loaded, + 1
 #ifdef GDR_TEST_WAIT_LIMIT_NS
@@ -526,18 +531,28 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_const
         for (int i = 0; i < ST; ++i) { mbar_init(&full[i], 1); mbar_init(&empty[i], Lay::kSplit ? 2 : 1); }
         for (int i = 0; i < 2 * A; ++i) { mbar_init(&acc_full[i], 1); mbar_init(&acc_empty[i], Lay::kSplit ? 8 : 16); }
         for (int i = 0; i < 2; ++i) { mbar_init(&slot_full[i], 4); mbar_init(&slot_free[i], 1); mbar_init(&drained[i], 1); }
+        mbar_init(&peer_tmem, 1);
         peers_plus_1 = 0;
         fence_mbar_init();
     }
     __syncwarp();
     cluster_sync();
-    if (warp == 9) tmem_alloc_pair(&tmem_slot, 512);
-    tc_fence_before_sync();
-    __syncthreads();
-    tc_fence_after_sync();
-    const uint32_t tmem = tmem_slot;
+    // Waits, allocation, start of the next kernel: in this order, as in the few-token
+    // kernel.  peer_tmem: the odd CTA has allocated.
     pdl_wait();
-    pdl_launch_dependents();
+    if (warp == 9) {
+        tmem_alloc_pair(&tmem_slot, 512);
+        pdl_launch_dependents();
+        __syncwarp();
+        tc_fence_before_sync();
+        if (rank == 1 && lane == 0) mbar_arrive_cluster(cluster_addr(smem_u32(&peer_tmem), 0));
+    }
+    const auto tmem_ready = [&] {                            // warps 0-7, 9 and 10
+        tc_fence_before_sync();
+        asm volatile("bar.sync 1, 320;" ::: "memory");
+        tc_fence_after_sync();
+        return *(volatile uint32_t*)&tmem_slot;
+    };
 
     // registers: 256 threads x 216 + 128 x 72 = the launch's 384 x 168
     if (warp >= 8) asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
@@ -572,13 +587,15 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_const
         }
         __syncwarp();
     } else if (warp == 9 || warp == 10) {
+        const uint32_t tmem = tmem_ready();
         if (rank == 0) {
             // 128 columns at a time: of half `mine` in every group, or of every group
             // whose last bit is `mine`
             constexpr uint32_t idesc = idesc_e4m3_f32(256, 128);
             const int mine = warp - 9;
             int i = 0, s = 0, phase = 0;
-            bool ok = true;
+            bool ok = wait(&peer_tmem, 0);
+            tc_fence_after_sync();
             for (int t = pair; t < tiles && ok; t += pairs) {
                 for (int g = 0; g < groups; ++g, ++i) {
                     if (Lay::kSplit || (i & 1) == mine) {
@@ -662,7 +679,6 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_const
         asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
         const int half = warp >> 2;                          // columns half * H .. + H - 1 of the tile
         const int row = (warp & 3) * 32 + lane;              // row of the CTA's 128
-        const uint32_t at0 = tmem + ((uint32_t)((warp & 3) * 32) << 16) + half * H;
         uint8_t* slot = smem + Lay::kSlots + half * Lay::kSlotBytes;
         const int side = Lay::kSplit ? half : 0;
         const uint32_t bars = cluster_addr(smem_u32(&acc_empty[side]), 0);
@@ -700,6 +716,7 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_const
             pair_tile(pair, tiles_m, tiles_n, &tm, &tn);
             enter();
         }
+        const uint32_t at0 = tmem_ready() + ((uint32_t)((warp & 3) * 32) << 16) + half * H;
         for (int t = pair; t < tiles && ok; t += pairs) {
             const int c_out = c0, m_tile = m0;
             const bool wide = ranges.wide(c_out, H);
@@ -787,7 +804,7 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_const
     }
     __syncthreads();
     cluster_sync();
-    if (warp == 9) tmem_dealloc_pair(tmem, 512);
+    if (warp == 9) tmem_dealloc_pair(tmem_slot, 512);
     __syncwarp();
     cluster_sync();
 }

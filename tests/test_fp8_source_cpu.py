@@ -1,6 +1,6 @@
 """Rules of the 8-bit product's kernels that no run on a healthy GPU shows, held on
 the source text (linear_fp8.cu): where they break, a kernel that gives up a wait
-would release memory that is still written."""
+would release memory that is still written, or two kernels would wait for each other."""
 import os
 import re
 
@@ -40,3 +40,21 @@ def test_mmas_and_their_commits_are_issued_by_the_elected_lane(call):
     assert places
     for at in places:
         assert any("elect_one()" in c for c in _enclosing_ifs(src, at)), src[at - 80:at + 40]
+
+
+@pytest.mark.parametrize("kernel", ["linear_few_kernel", "linear_pair_kernel"])
+def test_tensor_memory_is_held_only_after_the_previous_kernel(kernel):
+    """A kernel that the next one may overlap could let it start before its own
+    allocation: were tensor memory taken before the wait for that kernel's end, each
+    would wait for the other.  For the same reason the kernel after this one may start
+    only once this one has its columns."""
+    src = _source()
+    body = src[src.index(kernel + "("):]
+    body = body[:body.index("__global__") if "__global__" in body else len(body)]
+    places = [[m.start() for m in re.finditer(p, body)]
+              for p in (r"\bpdl_wait\(\)", r"\btmem_alloc(_pair)?\(", r"\bpdl_launch_dependents\(\)")]
+    assert [len(p) for p in places] == [1, 1, 1]
+    wait, alloc, start = (p[0] for p in places)
+    assert wait < alloc < start
+    alloc_ifs, start_ifs = _enclosing_ifs(body, alloc), _enclosing_ifs(body, start)
+    assert alloc_ifs and alloc_ifs == start_ifs           # by the allocating warp, after it
