@@ -1,6 +1,7 @@
 // fp8.cuh -- the 8-bit format shared by the norm, gated-norm and weight
 // kernels: e4m3 codes in groups of 128 channels with one fp32 scale each,
-// scale = max(max |y|, 1e-12) / 448, code = y / scale rounded to nearest even.
+// scale = max(max |y|, 1e-12) / 448, code = y / scale rounded to nearest even (of
+// activations: y times 1 / scale to 2 ulp, see fp8_codes).
 #pragma once
 
 #include <cstdint>
@@ -90,7 +91,11 @@ __device__ __forceinline__ float fp8_scale(uint32_t amax_bits) {
 __device__ __forceinline__ float fp8_inverse(float scale) { return __fdividef(1.f, scale); }
 
 // Codes of eight values: y * (1 / scale), saturating (the rounding of 1 / scale
-// may lift the largest value a few fp32 steps above 448).
+// may lift the largest value a few fp32 steps above 448).  Off by up to 2^-21 of the
+// quotient (2^-22 the inverse, 2^-24 the product), far below the rounding of the y
+// that the norms give; the quotient itself (below) would cost them time: 32768 rows of
+// 4096 bf16 without a residual 117 us in a graph instead of 96, 8192 of 896 with one
+// 9.5 instead of 9.1.
 __device__ __forceinline__ uint2 fp8_codes(const float* y, float inv_scale) {
     uint32_t h[4];
 #pragma unroll

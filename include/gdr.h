@@ -502,14 +502,21 @@ gdr_status gdr_decode_accept(int batch, int n_tokens, int n_heads, int d_k, int 
  * column is shorter when the width is no multiple of 128.  Every group has one
  * fp32 scale
  *     s = max(max |y|, 1e-12) / 448
- * and stands for the values s * code, with code = y / s rounded to the nearest
- * e4m3 value (ties to even).  A group that holds a NaN has scale NaN and NaN
+ * and stands for the values s * code, with code the e4m3 value nearest to a
+ * quotient (ties to even):
+ *     weights      y / s as fp32 rounds it
+ *     activations  y * r with r = 1 / s to 2 ulp, so y / s to 2^-21 of its size:
+ *                  a y / s that close to the border between two codes may get
+ *                  either
+ * A group that holds a NaN has scale NaN and NaN
  * codes; one that holds an infinity has an infinite scale, codes 0 for its
  * finite values and NaN for the infinite ones.
  *     activations  codes [rows, width], scales [rows, ceil(width / 128)]
  *     weights      codes [N, K],        scales [ceil(N / 128), ceil(K / 128)]
- * All sums and products before the rounding are fp32.  Rows, widths, N and K
- * are at most 2^31 - 1024 (GDR_ERR_INVALID_ARG above).
+ * All sums and products before the rounding are fp32; the norms' 1 / sqrt is
+ * good to 2 ulp.  A row (a head) whose squares add up past fp32's range comes out
+ * as zeros.  Rows, widths, N and K are at most 2^31 - 1024 (GDR_ERR_INVALID_ARG
+ * above).
  * ---------------------------------------------------------------------- */
 
 /* RMSNorm of the residual stream with the residual's addition:
@@ -544,6 +551,8 @@ gdr_status gdr_norm_fp8(const gdr_norm_fp8_args* args, void* stream);
 /* The mixer's output epilogue (as gdr_prefill_args.gate_raw) with 8-bit codes
  * as its result, from outputs that were computed without it: per token and head
  *     y = o / sqrt(mean_c o_c^2 + norm_eps) * norm_weight * sigmoid(gate_raw)
+ * sigmoid(g) is 1 / (1 + 2^(-g log2 e)) by the GPU's power and reciprocal, good to
+ * (8 + 2.4 |g|) 2^-24 of its size, and 0 below 2^-126.
  * The codes' groups run over the token's H * d_v channels (at d_v 64 a group
  * holds two heads).  o may be a prefill's (bf16 or fp32) or a decode step's
  * (fp32) output. */
