@@ -500,8 +500,10 @@ intra_chunk_kernel(const int32_t* __restrict__ cu, int n_seqs, int H,
         mbar_init(&in_bar[1], 1);
         fence_mbar_init();
     }
-    if (warp == 0) tmem_alloc(&tmem_slot, kTmemCols);
     pdl_wait();                               // the previous kernel's memory is final
+    // not before the wait: a previous kernel that lets this one start before its own
+    // allocation would wait for these columns, and this kernel for its end
+    if (warp == 0) tmem_alloc(&tmem_slot, kTmemCols);
 
     // Persistent CTA: items blockIdx.x, blockIdx.x + gridDim.x, ...  The next
     // item's inputs are staged while the current one is finished, and each
