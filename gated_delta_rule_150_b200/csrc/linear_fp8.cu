@@ -116,8 +116,10 @@ __device__ __forceinline__ void st_async4(uint32_t cluster_dst, const float4& v,
 // q % split), which adds the parts in rank order and stores.  The parts arrive in
 // a place of their own and are counted on a barrier, so nobody waits for the
 // whole cluster before its sums: no atomics, no workspace.  Bound by load latency and
-// by launches where K is short (one token, 3598 x 896: 2.9 us), by HBM and the way to
-// it where the weights are large (one token, 16416 x 4096: 13.7 us, 4.9 TB/s).
+// by launches where K is short (one token, 3598 x 896: 3.2 us, 2.5 with the weights in
+// L2), by HBM and the way to it where the weights are large (one token, 16416 x 4096:
+// 13.4 us, 5.0 TB/s).  Times here and at the choices of kernels below: graphs of calls
+// whose operands rotate past L2.
 //   warps 0-3   a thread owns an output column, BN fp32 sums (one per token)
 //   warp 4      TMA loads
 //   warp 5      TMEM allocation, MMAs
@@ -356,12 +358,11 @@ linear_few_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_consta
 // columns (commit, sums, arrival at the even CTA: about 750 cycles) has to fit into
 // the MMA time of the rest of TMEM.  At NT 256 (two accumulators) it bounds the
 // kernel; each half of an accumulator has its own barriers and issuing warp there, so
-// that a half waits for itself only (8192 x 4096 x 4096: 114 us, whole accumulators
-// 117).  At NT 128 (four) the 24 KB a group that a CTA takes in at about 61 bytes a
-// cycle do.  NT 128 is for products whose tiles do not fill the SMs (512 x 4096 x
-// 4096: 13.3 us against 17.4; 8192 x 4096 x 4096: 139 against 114).  Long runs are
-// held at 1.3 GHz by the power limit.  Persistent: a pair takes tiles a grid stride
-// apart.
+// that a half waits for itself only (whole accumulators were 3 % slower).  At NT 128
+// (four) the 24 KB a group that a CTA takes in at about 61 bytes a cycle do.  NT 128 is
+// for products whose tiles do not fill the SMs (512 x 4096 x 4096: 13.4 us against
+// 16.6; 8192 x 4096 x 4096: 159 against 127).  Long runs are held at 1.3 GHz by the
+// power limit.  Persistent: a pair takes tiles a grid stride apart.
 // ---------------------------------------------------------------------------
 constexpr int kPairThreads = 384;
 constexpr int kPairRowGroup = 8;                             // token tiles that take their column tiles together
@@ -432,8 +433,9 @@ struct RangeLane {
         return __any_sync(0xffffffffu, f32 && begin < c0 + cols && end > c0);
     }
     // The range that a slot of outputs goes to by TMA (`cols` columns from c0, all in
-    // one range with a map, at a 16-byte boundary of its rows), or -1.  What lies past
-    // the last range's columns is dropped by the store.
+    // one range with a map, at a 16-byte boundary of its rows, where a TMA store has to
+    // start, and not before the range, where it may not), or -1.  What lies past the
+    // last range's columns is dropped by the store.
     __device__ __forceinline__ int slot_range(bool is_wide, int c0, int cols) const {
         const bool mine = begin <= c0 && c0 < end && (c0 + cols <= end || last) && f32 == is_wide && mapped &&
                           ((c0 - begin) * (is_wide ? 4 : 2) & 15) == 0;
@@ -894,9 +896,11 @@ cudaError_t launch_few(const gdr_linear_fp8_args& a, EncodeTiledFn enc, cudaStre
     const int64_t token_tiles = (a.rows + BN - 1) / BN;
     if (token_tiles > 65535) return cudaErrorInvalidValue;
     // K in a power of two of parts, none without work: as many as fill the SMs once
-    // (4096 x 4096 for one token: 5.2 us, filled twice 6.3; the next kernel's start
-    // then overlaps this one), and twice where a CTA would have 16 groups or more of
-    // 64 tokens to add up (36 x 16416 x 4096: 17.0 against 19.1 us).
+    // (4096 x 4096 for one token: 5.7 us, filled twice 7.3; for 36 tokens, eight groups
+    // a CTA, 7.9 and 9.4; the next kernel's start then overlaps this one), and twice
+    // where a CTA would otherwise have 32 groups or more of 64 tokens to add up (16416
+    // columns for 36 tokens, K 8192: 27.8 against 32.9 us; K 4096, where the groups
+    // just reach that, 17.2 against 17.7, but 19.6 against 18.7 for 64 tokens).
     int split = 1;
     while (split < 8 && 2 * split <= groups) {
         const int64_t ctas = 2 * split * tiles * token_tiles;
@@ -945,10 +949,10 @@ cudaError_t launch_linear_fp8(const gdr_linear_fp8_args& a, cudaStream_t st) {
     if (a.rows <= 16) return launch_few<16>(a, enc, st);
     if (a.rows <= 32) return launch_few<32>(a, enc, st);
     // Up to 64 tokens, and more while the tiles of 64 tokens x 128 columns fill no more
-    // than half of the SMs (K is then split: 128 x 4096 x 4096 11.3 us, on CTA pairs
-    // 13.3), or all of them where K is short (256 x 3598 x 896: 6.2 against 7.3 us; 256 x
-    // 4096 x 4096: 17.1 against 13.3).  Beyond that each weight would be fetched again
-    // for every 64 tokens (256 x 16416 x 4096: 51 us against 20).
+    // than half of the SMs (K is then split: 128 x 4096 x 4096 12.0 us, on CTA pairs
+    // 12.7), or all of them where K is short (256 x 3598 x 896: 6.4 against 7.1 us; 256 x
+    // 4096 x 4096: 17.4 against 12.9).  Beyond that each weight would be fetched again
+    // for every 64 tokens (256 x 16416 x 4096: 60 us against 22).
     const int64_t small_tiles = fp8_groups(a.n) * ((a.rows + 63) / 64);
     if (a.rows <= 64 || small_tiles <= kSms / 2 || (small_tiles <= kSms && fp8_groups(a.k) <= 12))
         return launch_few<64>(a, enc, st);

@@ -103,8 +103,8 @@ norm_fp8_kernel(int rows, int width, const T* x, const T* residual, const float*
 // Eight lanes own one group of 128 channels of a token (one head at D 128, two at
 // D 64), 16 channels each: half the shuffles and divisions per channel of eight
 // channels a lane.  Bound by HBM with the issue slots close behind (16384 tokens of
-// 32 x 128, bf16: 65 us in a stream of calls or 0.79 of the copy rate; 82 us with eight
-// channels a lane, 71 before the arithmetic went two channels to an instruction).
+// 32 x 128, bf16: 66 us in a stream of calls or 0.78 of the copy rate, 62 in a graph;
+// in the stream 82 us with eight channels a lane, 71 with one channel to an instruction).
 // ---------------------------------------------------------------------------
 constexpr int kGatedThreads = 128;
 
@@ -121,10 +121,10 @@ __device__ __forceinline__ float rcp_approx(float x) {
 }
 
 // CTAs per SM that the registers have to leave room for: eight, at which all loads are
-// issued before the first is used (16384 x 7 x 64 with fp32 gates: 10.5 us, 12.9 when
-// the compiler chooses; 8192 x 32 x 128 with fp32 o: 39.6 against 41.9; 2048 x 14 x 64
-// bf16: 3.8 against 4.3), and ten for bf16 heads of 128, where more warps hide more
-// (16384 x 32 x 128: 60.3 us in a graph, 63.6 with eight).
+// issued before the first is used (in graphs, inputs rotating past L2: 16384 x 7 x 64
+// with fp32 gates 10.0 us, 12.0 when the compiler chooses; 8192 x 32 x 128 with fp32 o
+// 41.5 against 43.5; 2048 x 14 x 64 bf16 3.7 against 4.2), and ten for bf16 heads of
+// 128, where more warps hide more (16384 x 32 x 128: 62.1 us, 65.5 with eight).
 template <typename TO, typename TG, int D>
 constexpr int gated_ctas() { return sizeof(TO) + sizeof(TG) == 4 && D == 128 ? 10 : 8; }
 
@@ -196,8 +196,9 @@ gated_norm_fp8_kernel(int64_t tasks, int groups, int n16, const TO* __restrict__
 
 // ---------------------------------------------------------------------------
 // Weights: one CTA per 128 x 128 block, 16 threads across a row, 8 rows each
-// (16416 x 4096 bf16: 31.0 us, 0.99 of the copy rate, with four CTAs per SM; 33.7 with
-// three, 39 with the two that the registers would leave otherwise).
+// (16416 x 4096 bf16: 34.8 us or 0.88 of the copy rate in a stream of calls; in a graph
+// on matrices rotating past L2 33.0 with four CTAs per SM, 35.5 with three, 42.0 with
+// the two that the registers would leave otherwise).
 // ---------------------------------------------------------------------------
 constexpr int kQuantThreads = 256;
 
@@ -250,14 +251,14 @@ cudaError_t launch_norm_shape(const gdr_norm_fp8_args& a, int threads, cudaStrea
                       (T*)a.residual_out, (uint8_t*)a.y, a.y_scale);
 }
 
-// Two octets a thread: 8192 rows of 896 take 10.4 us with 64 threads a row, 11.5
-// with one warp of four octets, 11.3 with 128 of one; 65536 rows of 2048 take 139
-// us (1.03 of the copy rate) with 128 threads, 145 with a warp, 157 with 256.  Several
-// rows to a CTA of 256 threads are slower (16384 rows of 896: 22.1 against 20.5 us): they
-// load and wait together.  With too few rows to fill the SMs one octet a thread (a single
-// row of 896: 2.2 against 2.4 us).  Rows of one group would leave half of a warp idle:
-// two to a warp (65536 rows of 64: 10.1 against 20.2 us; 100000 of 128: 16.8 against
-// 30.4).
+// Two octets a thread (graphs of calls on inputs rotating past L2, bf16 with residual):
+// 65536 rows of 2048 take 142 us with 128 threads a row, 152 with a warp, 165 with 256;
+// at 8192 rows of 896 it makes no difference (64 threads 12.0 us, one warp of four
+// octets 12.4, 128 of one 11.8).  Several rows to a CTA of 256 threads were 8 % slower:
+// they load and wait together.  With too few rows to fill the SMs one octet a thread (a
+// single row of 896: 1.6 against 2.0 us).  Rows of one group would leave half of a warp
+// idle: two to a warp (65536 rows of 64: 10.0 against 20.3 us; 100000 of 128: 16.5
+// against 30.2).
 template <typename T, bool RES>
 cudaError_t launch_norm_typed(const gdr_norm_fp8_args& a, cudaStream_t st) {
     const int n8 = a.width / 8;

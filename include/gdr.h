@@ -541,7 +541,8 @@ typedef struct {
 
 /*
  * Enqueue the norm.  x, residual, norm_weight, residual_out and y must be
- * 16-byte aligned.  rows == 0 is a no-op.  Errors: GDR_ERR_INVALID_ARG (null or
+ * 16-byte aligned; outputs must overlap neither each other nor an input, but for
+ * residual_out as said above.  rows == 0 is a no-op.  Errors: GDR_ERR_INVALID_ARG (null or
  * misaligned pointer, bad size or dtype, residual_out without residual,
  * norm_eps negative or not finite), GDR_ERR_UNSUPPORTED (width no multiple of
  * 16 or above GDR_NORM_MAX_WIDTH), GDR_ERR_CUDA on a failed launch.
@@ -572,7 +573,7 @@ typedef struct {
 
 /*
  * Enqueue the gated norm.  o, gate_raw, norm_weight and y must be 16-byte
- * aligned.  rows == 0 is a no-op.  Errors as for gdr_norm_fp8
+ * aligned; outputs must overlap neither each other nor an input.  rows == 0 is a no-op.  Errors as for gdr_norm_fp8
  * (GDR_ERR_UNSUPPORTED: d_v not 64 or 128; the limit above
  * holds for H * d_v).
  */
@@ -584,7 +585,8 @@ gdr_status gdr_gated_norm_fp8(const gdr_gated_norm_fp8_args* args, void* stream)
  *   codes    device [n, k] e4m3 (output)
  *   scales   device [ceil(n / 128), ceil(k / 128)] (output)
  * n >= 0 rows (0 is a no-op); k a multiple of 16 (else GDR_ERR_UNSUPPORTED),
- * at least 16.  w and codes must be 16-byte aligned.
+ * at least 16.  w and codes must be 16-byte aligned; outputs must overlap neither
+ * each other nor w.
  */
 gdr_status gdr_quantize_weight_fp8(int n, int k, gdr_dtype w_dtype, const void* w, void* codes,
                                    float* scales, void* stream);
