@@ -65,24 +65,26 @@ def build(force: bool = False, verbose: bool = False, out: str = LIB, extra=()) 
 
 # A copy of the library for the bounded-wait tests: the state-pass kernels wait,
 # at their second chunk, for a barrier nothing arrives on, with a 1 ms limit, and
-# the 8-bit matrix product's MMA warps at their second group, with some 2 ms, so
-# that the timeout paths (error word, drain, GDR_ERR_TIMEOUT) run on demand.
+# one role of the 8-bit matrix product (the MMA warps by default) at its second
+# group, with some 2 ms, so that the timeout paths (error word, drain,
+# GDR_ERR_TIMEOUT) run on demand; csrc/testing holds what only this copy has.
 # Everything else is the regular library's objects.
 WAIT_TEST_LIB = os.path.join(OUT_DIR, "libgdr_waittest.so")
 WAIT_TEST_DEFINES = ["-DGDR_TEST_WAIT_LIMIT_NS=1000000"]
 WAIT_TEST_SOURCES = ["state_pass.cu", "linear_fp8.cu"]
+WAIT_TEST_EXTRA = [os.path.join(CSRC, "testing", "hold_tmem.cu")]
 
 
 def build_wait_test(force: bool = False) -> str:
     build()
-    if not force and not _stale(WAIT_TEST_LIB, sources()):
+    if not force and not _stale(WAIT_TEST_LIB, sources(WAIT_TEST_EXTRA)):
         return WAIT_TEST_LIB
     vdir = os.path.join(OUT_DIR, "waittest")
     os.makedirs(vdir, exist_ok=True)
     objs = []
-    for src in sources():
+    for src in sources(WAIT_TEST_EXTRA):
         name = os.path.splitext(os.path.basename(src))[0] + ".o"
-        if os.path.basename(src) not in WAIT_TEST_SOURCES:
+        if os.path.basename(src) not in WAIT_TEST_SOURCES and src not in WAIT_TEST_EXTRA:
             objs.append(os.path.join(OUT_DIR, name))
             continue
         vobj = os.path.join(vdir, name)

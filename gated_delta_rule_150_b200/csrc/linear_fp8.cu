@@ -191,7 +191,14 @@ linear_few_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_consta
     };
     if (warp == 4) {
         int i = 0;
+        // the first loads need no TMEM; no wait with a limit starts before it is there
+        bool allocated = false;
+        const auto after_alloc = [&] {
+            if (!allocated) asm volatile("bar.sync 2, 192;" ::: "memory");
+            allocated = true;
+        };
         for (int s = 0, phase = 1; i < count; ++i) {
+            if (i == ST) after_alloc();
             if (GDR_TEST_STALLS(1, i) || (part % 2 == 1 && GDR_TEST_STALLS(2, i)) ||
                 (i >= ST && !wait(&empty[s], phase))) break;
             if (elect_one()) {
@@ -204,6 +211,7 @@ linear_few_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_consta
             if (++s == ST) { s = 0; phase ^= 1; }
         }
         // no copy may still be in flight when the CTA ends, whichever role gave up
+        after_alloc();
         for (int j = i < ST ? 0 : i - ST; j < i; ++j) drain_wait(&full[j % ST], (j / ST) & 1);
     } else if (warp == 5) {
         constexpr uint32_t idesc = idesc_e4m3_f32(128, BN);
@@ -211,7 +219,7 @@ linear_few_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_consta
         pdl_launch_dependents();                             // not before: the next kernel may want TMEM too
         __syncwarp();
         tc_fence_before_sync();
-        asm volatile("bar.arrive 2, 160;" ::: "memory");     // for warps 0-3
+        asm volatile("bar.arrive 2, 192;" ::: "memory");     // for the other warps
         const uint32_t tmem = *(volatile uint32_t*)&tmem_slot;
         for (int i = 0, s = 0, phase = 0; i < count; ++i) {
             const int buf = (unsigned)i % kFewAccs;
@@ -257,7 +265,7 @@ linear_few_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_consta
         };
         fetch(g0);
         const OutColumn o(out, n0 + threadIdx.x);    // while the first loads are on their way
-        asm volatile("bar.sync 2, 160;" ::: "memory");       // warp 5 has allocated
+        asm volatile("bar.sync 2, 192;" ::: "memory");       // warp 5 has allocated
         tc_fence_after_sync();
         const uint32_t tmem = *(volatile uint32_t*)&tmem_slot;
         for (int i = 0; i < count; ++i) {
@@ -514,7 +522,7 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_const
     uint8_t* smem = align_smem<1024>(dyn);
     __shared__ uint64_t full[ST], empty[ST];
     __shared__ uint64_t acc_full[2 * A], acc_empty[2 * A];   // 2 * accumulator + half (not split: half 0 for both)
-    __shared__ uint64_t slot_full[2], slot_free[2], drained[2], peer_tmem;
+    __shared__ uint64_t slot_full[2], slot_free[2], drained[2];
     __shared__ uint32_t tmem_slot;
     __shared__ int peers_plus_1;                             // even CTA: groups that the odd one loaded, + 1
 #ifdef GDR_TEST_WAIT_LIMIT_NS
@@ -533,25 +541,24 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_const
         for (int i = 0; i < ST; ++i) { mbar_init(&full[i], 1); mbar_init(&empty[i], Lay::kSplit ? 2 : 1); }
         for (int i = 0; i < 2 * A; ++i) { mbar_init(&acc_full[i], 1); mbar_init(&acc_empty[i], Lay::kSplit ? 8 : 16); }
         for (int i = 0; i < 2; ++i) { mbar_init(&slot_full[i], 4); mbar_init(&slot_free[i], 1); mbar_init(&drained[i], 1); }
-        mbar_init(&peer_tmem, 1);
         peers_plus_1 = 0;
         fence_mbar_init();
     }
     __syncwarp();
     cluster_sync();
-    // Waits, allocation, start of the next kernel: in this order, as in the few-token
-    // kernel.  peer_tmem: the odd CTA has allocated.
+    // Wait, allocation, start of the next kernel: in this order, as in the few-token
+    // kernel.  Every warp takes up both CTAs' allocation (tmem_ready) before its first
+    // wait with a limit and after what needs no TMEM.
     pdl_wait();
     if (warp == 9) {
         tmem_alloc_pair(&tmem_slot, 512);
         pdl_launch_dependents();
         __syncwarp();
-        tc_fence_before_sync();
-        if (rank == 1 && lane == 0) mbar_arrive_cluster(cluster_addr(smem_u32(&peer_tmem), 0));
     }
-    const auto tmem_ready = [&] {                            // warps 0-7, 9 and 10
-        tc_fence_before_sync();
-        asm volatile("bar.sync 1, 320;" ::: "memory");
+    tc_fence_before_sync();
+    cluster_arrive();
+    const auto tmem_ready = [&] {
+        cluster_wait();
         tc_fence_after_sync();
         return *(volatile uint32_t*)&tmem_slot;
     };
@@ -561,12 +568,17 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_const
     const auto wait = [](uint64_t* bar, uint32_t parity) { return warp_wait(bar, parity); };
     if (warp == 8) {
         int i = 0, s = 0, phase = 1;
-        bool ok = true;
+        bool ok = true, allocated = false;
+        const auto after_alloc = [&] {
+            if (!allocated) tmem_ready();
+            allocated = true;
+        };
         for (int t = pair; t < tiles && ok; t += pairs) {
             int tm, tn;
             pair_tile(t, tiles_m, tiles_n, &tm, &tn);
             const int m0 = tm * 256 + (int)rank * 128, n0 = tn * NT + (int)rank * 64;
             for (int g = 0; g < groups; ++g, ++i) {
+                if (i == ST) after_alloc();
                 if (GDR_TEST_STALLS(1, i) || GDR_TEST_STALLS(rank == 1 ? 2 : 5, i) ||
                     (i >= ST && !wait(&empty[s], phase))) { ok = false; break; }
                 if (elect_one()) {
@@ -581,6 +593,7 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_const
                 if (++s == ST) { s = 0; phase ^= 1; }
             }
         }
+        after_alloc();
         // the last stages' releases must have landed before this CTA's shared memory goes
         for (int j = i < ST ? 0 : i - ST; j < i && ok; ++j) ok = wait(&empty[j % ST], (j / ST) & 1);
         if (lane == 0) {
@@ -596,8 +609,7 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_const
             constexpr uint32_t idesc = idesc_e4m3_f32(256, 128);
             const int mine = warp - 9;
             int i = 0, s = 0, phase = 0;
-            bool ok = wait(&peer_tmem, 0);
-            tc_fence_after_sync();
+            bool ok = true;
             for (int t = pair; t < tiles && ok; t += pairs) {
                 for (int g = 0; g < groups; ++g, ++i) {
                     if (Lay::kSplit || (i & 1) == mine) {
@@ -640,6 +652,7 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_const
             pending = -1;
         };
         const RangeLane ranges(out, maps, lane);
+        tmem_ready();
         for (int t = pair; t < tiles && ok; t += pairs) {
             int tm, tn;
             pair_tile(t, tiles_m, tiles_n, &tm, &tn);
