@@ -595,8 +595,9 @@ gdr_status gdr_quantize_weight_fp8(int n, int k, gdr_dtype w_dtype, const void* 
  *     y[m, c] = sum_b x_scale[m, b] w_scale[c / 128, b] sum_{j in group b} x[m, j] w[c, j]
  * The products of a group of 128 are summed by the tensor core in fp32, the
  * groups in fp32 registers in order of b (where the sum is split over CTAs,
- * the parts are added in order).  The result is rounded once to the output's
- * dtype, and equal inputs give equal bits.
+ * the parts are added in order).  The two scales of a group are multiplied first,
+ * in fp32, and their product has to lie within its range.  The result is rounded
+ * once to the output's dtype, and equal inputs give equal bits.
  *
  * The n output columns are cut into n_outs consecutive ranges, each written to
  * a dense tensor of its own: one product over the stacked weights of several

@@ -41,12 +41,14 @@ def _stop(libs, role, rows, n, k):
     assert T.gdr_linear_fp8_test_role(role) == 0
     torch.cuda.synchronize()
     assert T.gdr_linear_fp8_test_word() in (0, 1)
-    t0 = time.monotonic()
-    assert T.gdr_linear_fp8(ctypes.byref(plan.args), st) == OK
-    torch.cuda.synchronize()
-    took = time.monotonic() - t0
-    assert T.gdr_linear_fp8_test_word() == 1              # given up, and all of it seen to end
-    assert took < 1.0                                     # a wait for what never comes takes two seconds
+    took = []
+    for _ in range(2):                                    # the first call also loads the kernel
+        t0 = time.monotonic()
+        assert T.gdr_linear_fp8(ctypes.byref(plan.args), st) == OK
+        torch.cuda.synchronize()
+        took.append(time.monotonic() - t0)
+        assert T.gdr_linear_fp8_test_word() == 1          # given up, and all of it seen to end
+    assert min(took) < 1.0                                # a wait for what never comes takes two seconds
     assert T.gdr_linear_fp8(ctypes.byref(plan.args), st) == OK
     torch.cuda.synchronize()
     assert T.gdr_linear_fp8_status(st) == TIMEOUT and T.gdr_linear_fp8_status(st) == OK
