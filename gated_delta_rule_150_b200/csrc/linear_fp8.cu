@@ -60,7 +60,7 @@ struct OutColumn {
 // path: with a look at the timer in it the many-token kernel ran 10 to 30 %
 // slower, with one more store after the limit 2 to 4 %.
 #ifdef GDR_TEST_WAIT_LIMIT_NS
-constexpr int kWaitTries = 1 << 11;      // the test copy: its MMA warps wait for what nothing sends
+constexpr int kWaitTries = 1 << 11;      // the test copy
 #else
 constexpr int kWaitTries = 1 << 20;
 #endif
